@@ -16,7 +16,8 @@ ROOT = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG_DIR, "libbq.so")
-SOURCES = ["bq_api.hip", "qmv_u1.hip", "qmv_u2.hip", "qmv_t5.hip", "qmm_u1.hip", "qmm_u2.hip", "qmm_t5.hip"]
+SOURCES = ["bq_api.hip", "qmv_u1.hip", "qmv_u2.hip", "qmv_t5.hip", "qmm_u1.hip", "qmm_u2.hip", "qmm_t5.hip",
+           "kv_cache.hip", "kv_attn.hip", "kv_pages.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

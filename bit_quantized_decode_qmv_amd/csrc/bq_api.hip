@@ -240,18 +240,18 @@ const char* bq_strerror(int status) {
     case BQ_OK: return "success";
     case BQ_ERR_NULL: return "a required pointer is NULL";
     case BQ_ERR_BITS:
-      return "bits (1, 2, or BQ_BITS_T5 = 0) or the logits dtype is not valid for this entry point";
+      return "bits (1, 2, or BQ_BITS_T5 = 0), the logits dtype or the cache format is not valid for this entry point";
     case BQ_ERR_GROUP: return "group_size must be 64 or 128";
     case BQ_ERR_SHAPE:
       return "N and K must be positive, K a multiple of group_size, and the sizes within the limits of bq.h";
     case BQ_ERR_M: return "M is outside the range this entry point accepts";
     case BQ_ERR_ALIGN:
       return "a pointer is misaligned (W 4 bytes; x, scales and biases of the decode calls 4 bytes; x and the "
-             "workspace of the prefill products 16 bytes; fp16 outputs 2 bytes), or a t5 repack has K not a "
-             "multiple of 256";
+             "workspace of the prefill products 16 bytes; fp16 outputs 2 bytes; the cache's arrays and rows 16 bytes), "
+             "or a t5 repack has K not a multiple of 256";
     case BQ_ERR_FLAGS: return "flags holds bits this entry point does not define";
     case BQ_ERR_HIP: return "the HIP runtime rejected the kernel launch";
-    case BQ_ERR_WORKSPACE: return "the workspace is NULL or smaller than bq_spec_verify_workspace reports";
+    case BQ_ERR_WORKSPACE: return "the workspace is NULL or smaller than the call's workspace function reports";
     case BQ_ERR_SCRATCH:
       return "the call needs more scratch than the allocation-free entry point's static array "
              "(BQ_SPEC_NOALLOC_SCRATCH_BYTES) holds";

@@ -1,0 +1,372 @@
+"""Attention with a paged key/value cache in 8 bits: the binding of the
+``bq_rope`` and ``bq_kv_*`` entry points of ``include/bq.h`` and their tensor
+helpers (``rope``, ``kv_append``, ``kv_read``, ``kv_attn``, ``kv_fork``,
+``kv_resize``, ``kv_compact``, ``kv_copy_pages``) over a :class:`KVCache`.
+
+As in the rest of the package every step runs in the HIP kernels; a helper
+checks its arguments, allocates what it returns and passes the current stream.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+KV_PAGE = 64
+KV_BLOCK = 16
+KV_I8 = 1
+KV_E4M3 = 2
+KV_FORMATS = {"int8": KV_I8, "e4m3": KV_E4M3}
+KV_CAUSAL = 1
+KV_ATTN_COUNTER_BYTES = 65536
+ROPE_ADJACENT = 1
+ROPE_MAX_AXES = 8
+
+KV_POINTS = ("bq_rope", "bq_kv_append", "bq_kv_read", "bq_kv_attn_workspace", "bq_kv_attn", "bq_kv_pages_workspace",
+             "bq_kv_fork", "bq_kv_resize", "bq_kv_compact", "bq_kv_copy_pages")
+
+
+class KVCacheDesc(ctypes.Structure):
+    """bq_kv_cache of include/bq.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("layers", ctypes.c_int), ("num_pages", ctypes.c_int),
+                ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("format", ctypes.c_int)]
+
+
+def declare(lib) -> None:
+    """Argument types of the entry points."""
+    vp, i, ll, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_size_t
+    cache = ctypes.POINTER(KVCacheDesc)
+    size = ctypes.POINTER(sz)
+    types = {
+        "bq_rope": [vp, vp, ll, ll, i, i, i, vp, vp, vp, i, i, i, vp],
+        "bq_kv_append": [cache, i, vp, vp, ll, ll, vp, vp, ll, ll, i, vp, vp, vp, i, i, i, vp, vp, vp, i, i, i, vp],
+        "bq_kv_read": [cache, i, vp, vp, vp, vp, vp, i, i, i, vp],
+        "bq_kv_attn_workspace": [cache, i, i, i, size],
+        "bq_kv_attn": [cache, i, vp, vp, ll, ll, i, vp, vp, vp, i, i, i, ctypes.c_float, i, i, vp, sz, vp],
+        "bq_kv_pages_workspace": [cache, i, size],
+        "bq_kv_fork": [cache, vp, vp, vp, i, i, vp, vp, i, vp, vp, sz, vp],
+        "bq_kv_resize": [cache, vp, vp, vp, i, i, vp, vp, vp, sz, vp],
+        "bq_kv_compact": [cache, vp, vp, i, i, vp, vp, sz, vp],
+        "bq_kv_copy_pages": [cache, vp, vp, i, vp],
+    }
+    for name, args in types.items():
+        fn = getattr(lib, name)
+        fn.restype = ctypes.c_int
+        fn.argtypes = args
+
+
+def _pkg():
+    import bit_quantized_decode_qmv_amd as bq
+    return bq
+
+
+def _c_entry(name):
+    def fn(*args):
+        bq = _pkg()
+        return bq._raise_if(getattr(bq.load_library(), name)(*args), name)
+    fn.__name__ = name
+    fn.__doc__ = f"C entry point {name} of include/bq.h (pointers and stream as integers, the cache as KVCache.desc)."
+    return fn
+
+
+bq_rope = _c_entry("bq_rope")
+bq_kv_append = _c_entry("bq_kv_append")
+bq_kv_read = _c_entry("bq_kv_read")
+bq_kv_attn = _c_entry("bq_kv_attn")
+bq_kv_fork = _c_entry("bq_kv_fork")
+bq_kv_resize = _c_entry("bq_kv_resize")
+bq_kv_compact = _c_entry("bq_kv_compact")
+bq_kv_copy_pages = _c_entry("bq_kv_copy_pages")
+
+
+def bq_kv_attn_workspace(desc, q_heads, batch, total):
+    """Workspace bytes bq_kv_attn wants for its full split (host only)."""
+    n = ctypes.c_size_t(0)
+    bq = _pkg()
+    bq._raise_if(bq.load_library().bq_kv_attn_workspace(desc, q_heads, batch, total, ctypes.byref(n)),
+                 "bq_kv_attn_workspace")
+    return n.value
+
+
+def bq_kv_pages_workspace(desc, rows):
+    """Workspace bytes the page calls need (host only)."""
+    n = ctypes.c_size_t(0)
+    bq = _pkg()
+    bq._raise_if(bq.load_library().bq_kv_pages_workspace(desc, rows, ctypes.byref(n)), "bq_kv_pages_workspace")
+    return n.value
+
+
+class KVCache:
+    """A paged key/value cache in 8 bits over the caller's tensors:
+    k, v uint8 [layers][pages][kv_heads][64 * head_dim], k_scales, v_scales
+    float32 [layers][pages][kv_heads][4] (``include/bq.h`` gives the order of
+    a page's bytes).  format: "int8" or "e4m3"."""
+
+    __slots__ = ("k", "v", "k_scales", "v_scales", "format", "device", "layers", "num_pages", "kv_heads", "head_dim",
+                 "desc")
+
+    def __init__(self, k, v, k_scales, v_scales, format: str = "int8"):
+        bq = _pkg()
+        torch = bq._torch()
+        if format not in KV_FORMATS:
+            raise ValueError(f"format must be one of {sorted(KV_FORMATS)}, got {format!r}")
+        bq._check(k, "k", torch.uint8, None)
+        dev = k.device
+        bq._check(v, "v", torch.uint8, dev)
+        bq._check(k_scales, "k_scales", torch.float32, dev)
+        bq._check(v_scales, "v_scales", torch.float32, dev)
+        shape = k.shape
+        if len(shape) != 4 or shape[3] % KV_PAGE:
+            raise ValueError(f"k has shape {tuple(shape)}, expected [layers][pages][kv_heads][{KV_PAGE} * head_dim]")
+        if v.shape != shape:
+            raise ValueError(f"v has shape {tuple(v.shape)}, k {tuple(shape)}")
+        layers, pages, heads, row = shape
+        scales = (layers, pages, heads, KV_PAGE // KV_BLOCK)
+        if k_scales.shape != scales or v_scales.shape != scales:
+            raise ValueError(f"scales have shapes {tuple(k_scales.shape)}, {tuple(v_scales.shape)}, expected {scales}")
+        self.k, self.v, self.k_scales, self.v_scales, self.format = k, v, k_scales, v_scales, format
+        self.device = dev
+        self.layers, self.num_pages, self.kv_heads, self.head_dim = layers, pages, heads, row // KV_PAGE
+        self.desc = KVCacheDesc(k.data_ptr(), v.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), layers, pages,
+                                heads, row // KV_PAGE, KV_FORMATS[format])
+
+    @classmethod
+    def empty(cls, layers: int, num_pages: int, kv_heads: int, head_dim: int, format: str = "int8", device="cuda"):
+        """A cache of its own memory, uninitialised: tokens exist once they are appended."""
+        torch = _pkg()._torch()
+        codes = (layers, num_pages, kv_heads, KV_PAGE * head_dim)
+        scales = (layers, num_pages, kv_heads, KV_PAGE // KV_BLOCK)
+        return cls(*(torch.empty(codes, dtype=torch.uint8, device=device) for _ in range(2)),
+                   *(torch.empty(scales, dtype=torch.float32, device=device) for _ in range(2)), format=format)
+
+
+def _rows(t, name, device, heads=None, head_dim=None):
+    """Checks a row array [tokens][heads][head_dim], fp16, any row stride; returns its row stride."""
+    torch = _pkg()._torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be on the GPU, got {t.device}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != torch.float16:
+        raise TypeError(f"{name} must be torch.float16, got {t.dtype}")
+    shape = t.shape
+    if len(shape) != 3 or (heads is not None and shape[1] != heads) or (head_dim is not None and shape[2] != head_dim):
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected [tokens][{heads or 'heads'}][{head_dim or 'head_dim'}]")
+    s0, s1, s2 = t.stride()
+    row = shape[1] * shape[2]
+    if s2 != 1 or (s1 != shape[2] and shape[1] > 1):
+        raise ValueError(f"{name} must hold each row [heads][head_dim] contiguously")
+    if shape[0] <= 1:
+        return row  # a single row has no stride
+    if s0 < row:
+        raise ValueError(f"{name} has overlapping rows (stride {s0}, row {row})")
+    return s0
+
+
+def _batch(cu, lens, table, device):
+    bq = _pkg()
+    torch = bq._torch()
+    bq._check(cu, "cu", torch.int32, device)
+    bq._check(lens, "lens", torch.int32, device)
+    bq._check(table, "table", torch.int32, device)
+    n = lens.shape[0]
+    if lens.dim() != 1 or cu.dim() != 1 or cu.shape[0] != n + 1 or table.dim() != 2 or table.shape[0] != n:
+        raise ValueError(f"expected lens [batch], cu [batch + 1], table [batch][max_pages]; got {tuple(lens.shape)}, "
+                         f"{tuple(cu.shape)}, {tuple(table.shape)}")
+    return n, table.shape[1]
+
+
+def _angles(pos, inv_freq, axis, adjacent, tokens, device):
+    """(pos, inv_freq, axis pointers, rot_dim, axes, flags)"""
+    if inv_freq is None:
+        if pos is not None or axis is not None:
+            raise ValueError("pos and axis need inv_freq")
+        return None, None, None, 0, 1, 0
+    bq = _pkg()
+    torch = bq._torch()
+    bq._check(inv_freq, "inv_freq", torch.float32, device)
+    bq._check(pos, "pos", torch.int32, device)
+    rot = 2 * inv_freq.numel()
+    if pos.dim() == 1:
+        pos = pos[None]
+    if pos.dim() != 2 or pos.shape[1] != tokens:
+        raise ValueError(f"pos has shape {tuple(pos.shape)}, expected [axes][{tokens}]")
+    if axis is not None:
+        bq._check(axis, "axis", torch.int32, device)
+        if axis.numel() * 2 != rot:
+            raise ValueError(f"axis has {axis.numel()} values, inv_freq {inv_freq.numel()}")
+    return (pos.data_ptr(), inv_freq.data_ptr(), axis.data_ptr() if axis is not None else None, rot, pos.shape[0],
+            ROPE_ADJACENT if adjacent else 0)
+
+
+def _out(t, name, like, device):
+    if t is None:
+        bq = _pkg()
+        t = bq._torch().empty(like.shape, dtype=like.dtype, device=device)
+        return t, like.shape[1] * like.shape[2]
+    return t, _rows_like(t, name, like, device)
+
+
+def _rows_like(t, name, like, device):
+    stride = _rows(t, name, device, like.shape[1], like.shape[2])
+    if t.shape[0] != like.shape[0]:
+        raise ValueError(f"{name} has {t.shape[0]} rows, expected {like.shape[0]}")
+    return stride
+
+
+def rope(x, pos, inv_freq, axis=None, adjacent: bool = False, out=None):
+    """x [tokens][heads][head_dim] with its first 2 * len(inv_freq) dimensions
+    turned by pos[axis[r]][token] * inv_freq[r] (pair r: dimensions r and
+    r + rot/2; adjacent: 2r and 2r + 1).  pos int32 [axes][tokens] (or
+    [tokens]), inv_freq float32, axis int32 (None: the first axis for all).
+    out may be x."""
+    bq = _pkg()
+    stride = _rows(x, "x", None)
+    dev = x.device
+    tokens, heads, dim = x.shape
+    a = _angles(pos, inv_freq, axis, adjacent, tokens, dev)
+    out, out_stride = _out(out, "out", x, dev)
+    bq_rope(x.data_ptr(), out.data_ptr(), stride, out_stride, tokens, heads, dim, *a, bq._stream_handle(dev))
+    return out
+
+
+def kv_append(cache: KVCache, layer: int, k, v, cu, lens, table, q=None, pos=None, inv_freq=None, axis=None,
+              adjacent: bool = False, q_out=None):
+    """Writes the rows k, v [total][kv_heads][head_dim] to the cache as the
+    last tokens of their sequences (lens counts them), k turned as rope()
+    does; with q [total][q_heads][head_dim] also returns q turned (into q_out
+    when given).  Without inv_freq nothing turns."""
+    bq = _pkg()
+    dev = cache.device
+    total = k.shape[0]
+    k_stride = _rows(k, "k", dev, cache.kv_heads, cache.head_dim)
+    v_stride = _rows_like(v, "v", k, dev)
+    batch, max_pages = _batch(cu, lens, table, dev)
+    a = _angles(pos, inv_freq, axis, adjacent, total, dev)
+    qp = op = None
+    q_stride = out_stride = q_heads = 0
+    if q is not None:
+        q_stride = _rows(q, "q", dev, None, cache.head_dim)
+        if q.shape[0] != total:
+            raise ValueError(f"q has {q.shape[0]} rows, k {total}")
+        q_out, out_stride = _out(q_out, "q_out", q, dev)
+        qp, op, q_heads = q.data_ptr(), q_out.data_ptr(), q.shape[1]
+    bq_kv_append(cache.desc, layer, k.data_ptr(), v.data_ptr(), k_stride, v_stride, qp, op, q_stride, out_stride,
+                 q_heads, cu.data_ptr(), lens.data_ptr(), table.data_ptr(), batch, max_pages, total, *a,
+                 bq._stream_handle(dev))
+    return q_out if q is not None else None
+
+
+def kv_read(cache: KVCache, layer: int, cu, lens, table, total: int):
+    """(k, v) fp16 [total][kv_heads][head_dim]: the values held for the last
+    cu[b+1] - cu[b] tokens of each sequence; total = cu[-1]."""
+    bq = _pkg()
+    torch = bq._torch()
+    dev = cache.device
+    batch, max_pages = _batch(cu, lens, table, dev)
+    k = torch.empty((total, cache.kv_heads, cache.head_dim), dtype=torch.float16, device=dev)
+    v = torch.empty_like(k)
+    bq_kv_read(cache.desc, layer, k.data_ptr(), v.data_ptr(), cu.data_ptr(), lens.data_ptr(), table.data_ptr(), batch,
+               max_pages, total, bq._stream_handle(dev))
+    return k, v
+
+
+def kv_attn(cache: KVCache, layer: int, q, cu, lens, table, scale: Optional[float] = None, causal: bool = True,
+            window: int = 0, out=None, workspace=None):
+    """Attention of the rows q [total][q_heads][head_dim] over the cache; scale
+    defaults to head_dim ** -0.5.  causal: a row sees the tokens up to its own
+    position (the rows are the last of their sequence), window > 0: only the
+    last `window` of them; else every token held.  workspace: a uint8 tensor,
+    zero before its first use and kept for later calls (see
+    bq_kv_attn_workspace); allocated here when None."""
+    bq = _pkg()
+    dev = cache.device
+    stride = _rows(q, "q", dev, None, cache.head_dim)
+    total, heads, dim = q.shape
+    batch, max_pages = _batch(cu, lens, table, dev)
+    out, out_stride = _out(out, "out", q, dev)
+    if workspace is None:
+        torch = bq._torch()
+        need = bq_kv_attn_workspace(cache.desc, heads, batch, total)
+        workspace = torch.zeros(need, dtype=torch.uint8, device=dev) if need else None
+    else:
+        bq._check(workspace, "workspace", bq._torch().uint8, dev)
+    bq_kv_attn(cache.desc, layer, q.data_ptr(), out.data_ptr(), stride, out_stride, heads, cu.data_ptr(),
+               lens.data_ptr(), table.data_ptr(), batch, max_pages, total, dim ** -0.5 if scale is None else scale,
+               window, KV_CAUSAL if causal else 0, workspace.data_ptr() if workspace is not None else None,
+               workspace.numel() if workspace is not None else 0, bq._stream_handle(dev))
+    return out
+
+
+def _ints(t, name, device, shape):
+    bq = _pkg()
+    bq._check(t, name, bq._torch().int32, device)
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _page_call(name, cache, table, refs, workspace, *args):
+    """args: the tensors and sizes between rows, max_pages and status."""
+    bq = _pkg()
+    torch = bq._torch()
+    dev = cache.device
+    bq._check(table, "table", torch.int32, dev)
+    if table.dim() != 2:
+        raise ValueError(f"table has shape {tuple(table.shape)}, expected [rows][max_pages]")
+    _ints(refs, "refs", dev, (cache.num_pages,))
+    status = torch.empty(2, dtype=torch.int32, device=dev)
+    if workspace is None:
+        workspace = torch.empty(bq_kv_pages_workspace(cache.desc, table.shape[0]), dtype=torch.uint8, device=dev)
+    else:
+        bq._check(workspace, "workspace", torch.uint8, dev)
+    lens, *rest = args
+    bq._raise_if(getattr(bq.load_library(), name)(
+        cache.desc, table.data_ptr(), *([lens.data_ptr()] if lens is not None else []), refs.data_ptr(),
+        table.shape[0], table.shape[1], *rest, status.data_ptr(), workspace.data_ptr(), workspace.numel(),
+        bq._stream_handle(dev)), name)
+    return status
+
+
+def kv_fork(cache: KVCache, table, lens, refs, src, dst, workspace=None):
+    """Row dst[i] becomes a copy of row src[i]: whole pages shared, a partly
+    filled last page copied.  Updates table, lens, refs on the GPU and
+    returns status int32 [2] (0 / -1 invalid / pages short; pages copied)."""
+    _ints(lens, "lens", cache.device, table.shape[:1])
+    n = src.shape[0]
+    _ints(src, "src", cache.device, (n,))
+    _ints(dst, "dst", cache.device, (n,))
+    return _page_call("bq_kv_fork", cache, table, refs, workspace, lens, src.data_ptr(), dst.data_ptr(), n)
+
+
+def kv_resize(cache: KVCache, table, lens, refs, want, workspace=None):
+    """Row i gets the length want[i] (-1: as it is): pages are let go or
+    taken, a shared page that becomes the partly filled last one is copied.
+    Returns status as kv_fork."""
+    _ints(lens, "lens", cache.device, table.shape[:1])
+    _ints(want, "want", cache.device, table.shape[:1])
+    return _page_call("bq_kv_resize", cache, table, refs, workspace, lens, want.data_ptr())
+
+
+def kv_compact(cache: KVCache, table, refs, workspace=None):
+    """Moves pages so that those in use have the lowest ids; table and refs
+    follow.  Returns status as kv_fork (status[1]: pages moved)."""
+    return _page_call("bq_kv_compact", cache, table, refs, workspace, None)
+
+
+def kv_copy_pages(cache: KVCache, src, dst) -> None:
+    """Copies pages src[i] to dst[i] over all layers."""
+    bq = _pkg()
+    n = src.shape[0]
+    _ints(src, "src", cache.device, (n,))
+    _ints(dst, "dst", cache.device, (n,))
+    bq_kv_copy_pages(cache.desc, src.data_ptr(), dst.data_ptr(), n, bq._stream_handle(cache.device))
+
+
+__all__ = [
+    "KV_ATTN_COUNTER_BYTES", "KV_BLOCK", "KV_CAUSAL", "KV_E4M3", "KV_FORMATS", "KV_I8", "KV_PAGE", "KV_POINTS",
+    "KVCache", "KVCacheDesc", "ROPE_ADJACENT", "ROPE_MAX_AXES", "bq_kv_append", "bq_kv_attn", "bq_kv_attn_workspace",
+    "bq_kv_compact", "bq_kv_copy_pages", "bq_kv_fork", "bq_kv_pages_workspace", "bq_kv_read", "bq_kv_resize",
+    "bq_rope", "kv_append", "kv_attn", "kv_compact", "kv_copy_pages", "kv_fork", "kv_read", "kv_resize", "rope",
+]

@@ -67,7 +67,7 @@ extern "C" {
 typedef enum bq_status {
   BQ_OK = 0,
   BQ_ERR_NULL = -1,       /* a required pointer is NULL */
-  BQ_ERR_BITS = -2,       /* bits (or the logits dtype) not valid for this entry point */
+  BQ_ERR_BITS = -2,       /* bits (or the logits dtype, or the cache format) not valid for this entry point */
   BQ_ERR_GROUP = -3,      /* group_size not 64 or 128 */
   BQ_ERR_SHAPE = -4,      /* N or K not positive, K % group_size != 0, K > 2^26,
                              or N * (packed row bytes) >= 2^30, or
@@ -77,8 +77,10 @@ typedef enum bq_status {
   BQ_ERR_M = -5,          /* M outside the range this entry point accepts */
   BQ_ERR_ALIGN = -6,      /* a pointer is misaligned, or a t5 repack with K % 256 != 0 */
   BQ_ERR_HIP = -7,        /* the HIP runtime rejected a launch */
-  BQ_ERR_FLAGS = -8,      /* bq_linear: flags holds undefined bits */
-  BQ_ERR_WORKSPACE = -9,  /* bq_spec_decode_verify: workspace NULL or too small */
+  BQ_ERR_FLAGS = -8,      /* bq_linear, bq_rope, bq_kv_append, bq_kv_attn: flags holds
+                             undefined bits (or a window without BQ_KV_CAUSAL) */
+  BQ_ERR_WORKSPACE = -9,  /* bq_spec_decode_verify, bq_kv_fork / resize / compact:
+                             workspace NULL or too small */
   BQ_ERR_SCRATCH = -10    /* bq_spec_decode_verify_noalloc: the call needs more than
                              BQ_SPEC_NOALLOC_SCRATCH_BYTES of scratch */
 } bq_status;
@@ -310,6 +312,148 @@ int bq_spec_decode_verify(const void* logits, int logits_dtype, const int* draft
 #define BQ_SPEC_NOALLOC_SCRATCH_BYTES (2 * 1024 * 1024)
 int bq_spec_decode_verify_noalloc(const void* logits, int logits_dtype, const int* draft, int B, int L, int V,
                                   int* accepted, int* next_token, int* target_tokens, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Attention with a paged key/value cache held in 8 bits.
+ *
+ * The cache.  A page holds BQ_KV_PAGE = 64 tokens; every BQ_KV_BLOCK = 16
+ * tokens of a page share one scale per head, for K and for V:
+ *   k, v                 uint8 [layers][num_pages][kv_heads][64 * head_dim]
+ *   k_scales, v_scales   fp32  [layers][num_pages][kv_heads][4]
+ * value = scale * code.  format BQ_KV_I8: the code is an integer -127..127,
+ * held as the byte code + 128; BQ_KV_E4M3: the byte is an OCP e4m3 number.
+ * The bytes of a page lie in the order in which the matrix instructions take
+ * them:
+ *   K  [i: 4][c: head_dim/64][g: 4][t: 16][j: 16]  token 16i + t, dim 64c + 16g + j
+ *   V  [n: head_dim/16][g: 4][d: 16][i: 4][j: 4]   token 16i + 4g + j, dim 16n + d
+ * head_dim 64, 128, 192 or 256; kv_heads 1..1024; codes and scales 16-byte
+ * aligned.  layer selects one layer of the arrays; page calls work on all.
+ *
+ * The batch of a call.  Sequence b has the rows cu[b] .. cu[b+1] - 1 of the
+ * call's packed row arrays (cu: int32 [batch + 1], rising, cu[batch] =
+ * total), holds lens[b] tokens, and its token t lies in page
+ * table[b][t / 64] (int32 [batch][max_pages]).  Its rows are its last
+ * tokens: row i of n stands at position lens[b] - n + i.  All three arrays
+ * are device memory, read by the kernels only, so a captured call follows
+ * what they hold at each replay.  Entries that do not fit (cu past total,
+ * lens past 64 * max_pages, a page id outside 0 .. num_pages - 1) are never
+ * followed: such rows, tokens and pages count as absent.
+ *
+ * Row arrays are fp16 [total][heads][head_dim] with a stride in elements
+ * from row to row (at least heads * head_dim, a multiple of 8); pointers
+ * 16-byte aligned.  total == 0 is a call that does nothing (its row arrays
+ * may be NULL). */
+#define BQ_KV_PAGE 64
+#define BQ_KV_BLOCK 16
+#define BQ_KV_I8 1
+#define BQ_KV_E4M3 2
+#define BQ_KV_MAX_PAGES (1 << 24)
+
+typedef struct bq_kv_cache {
+  void* k;
+  void* v;
+  float* k_scales;
+  float* v_scales;
+  int layers, num_pages, kv_heads, head_dim, format;
+} bq_kv_cache;
+
+/* rope -- rotary positions with several axes (time, height, width of images
+ * and video; one axis for text).  Pair r of the first rot_dim dimensions of
+ * every head turns by a = pos[axis[r]][token] * inv_freq[r]:
+ *   y1 = x1 cos a - x2 sin a,  y2 = x2 cos a + x1 sin a,
+ * x1, x2 = dimensions r and r + rot_dim/2, or 2r and 2r + 1 with
+ * BQ_ROPE_ADJACENT; dimensions past rot_dim pass through.
+ * x, y: rows as above, y may be x (with the same stride); head_dim a multiple of 16 up to
+ * 1024, rot_dim a multiple of 16 up to head_dim (0: nothing turns, the
+ * arrays may be NULL); pos int32 [axes][tokens], inv_freq fp32
+ * [rot_dim/2], axis int32 [rot_dim/2] (NULL: all 0; values outside 0 ..
+ * axes - 1 are brought into it), 1 <= axes <= BQ_ROPE_MAX_AXES.  The angle
+ * is exact to 2^-20 turns at any position.  Undefined flag bits:
+ * BQ_ERR_FLAGS. */
+#define BQ_ROPE_ADJACENT 1
+#define BQ_ROPE_MAX_AXES 8
+int bq_rope(const void* x, void* y, long long x_stride, long long y_stride, int tokens, int heads, int head_dim,
+            const int* pos, const float* inv_freq, const int* axis, int rot_dim, int axes, int flags, void* stream);
+
+/* kv_append -- rotates the new rows' k (and q, when q is not NULL, into
+ * q_out) as bq_rope does and writes k and v to the cache as the last tokens
+ * of their sequences; lens already counts them.  Every block that takes a
+ * new token gets the scale
+ *   max(largest |new value| / 127 (e4m3: / 448), its scale if it holds older tokens),
+ * new values are coded as rne(value / scale), codes of the block's older
+ * tokens are brought to the new scale (unchanged when it did not grow), and
+ * tokens of the block past lens are cleared.  Infinities do not count for
+ * the scale and are held as the largest code, NaN as 0.  Writing the same
+ * rows again (after a rejected draft, say) replaces them.  Pages that
+ * several sequences share must not be written: bq_kv_fork and bq_kv_resize
+ * never leave a partly filled page shared. */
+int bq_kv_append(const bq_kv_cache* cache, int layer, const void* k, const void* v, long long k_stride,
+                 long long v_stride, const void* q, void* q_out, long long q_stride, long long q_out_stride,
+                 int q_heads, const int* cu, const int* lens, const int* table, int batch, int max_pages, int total,
+                 const int* pos, const float* inv_freq, const int* axis, int rot_dim, int axes, int flags,
+                 void* stream);
+
+/* kv_read -- the values held for the last tokens of each sequence, as
+ * contiguous fp16 [total][kv_heads][head_dim] (one rounding of
+ * scale * code); rows that no page holds are zero. */
+int bq_kv_read(const bq_kv_cache* cache, int layer, void* k, void* v, const int* cu, const int* lens, const int* table,
+               int batch, int max_pages, int total, void* stream);
+
+/* kv_attn -- out[row][h] = sum_j p_j v_j / sum_j p_j, p_j = exp(scale *
+ * q[row][h] . k_j), over the tokens j of the row's sequence that the row
+ * sees, with the key/value head h / (q_heads / kv_heads).  With BQ_KV_CAUSAL
+ * a row at position n sees j <= n, and with window > 0 only j > n - window;
+ * without it every row sees all lens[b] tokens (an encoder's states).  A row
+ * that sees nothing gives zeros.  Scores, sums and outputs in fp32, codes
+ * exact, probabilities rounded to fp16 for the product with V.
+ *
+ * workspace (device memory, 16-byte aligned, or NULL): lets the tokens of a
+ * long sequence be shared by several workgroups.  Its first
+ * BQ_KV_ATTN_COUNTER_BYTES must be zero before its first use; every call
+ * leaves them zero again.  bq_kv_attn_workspace gives the size of the full
+ * split; less gives a smaller split or none, with results that may differ
+ * in the last bits.  Calls that overlap in time must not share a workspace.
+ * One launch; the same bits on every call with the same arguments. */
+#define BQ_KV_CAUSAL 1
+#define BQ_KV_ATTN_COUNTER_BYTES 65536
+int bq_kv_attn_workspace(const bq_kv_cache* cache, int q_heads, int batch, int total, size_t* bytes);
+int bq_kv_attn(const bq_kv_cache* cache, int layer, const void* q, void* out, long long q_stride,
+               long long out_stride, int q_heads, const int* cu, const int* lens, const int* table, int batch,
+               int max_pages, int total, float scale, int window, int flags, void* workspace, size_t workspace_bytes,
+               void* stream);
+
+/* Pages.  table int32 [rows][max_pages], lens int32 [rows], refs int32
+ * [num_pages]: the number of table entries that hold a page; a page is free
+ * when it is 0.  Free pages are taken lowest first, in the order of the
+ * call's rows.  All arrays are device memory and are updated there; status
+ * (int32 [2], device) receives
+ *   status[0]  0 done; -1 an argument array holds something invalid; n > 0:
+ *              n more free pages are needed.  Unless 0, nothing was changed.
+ *   status[1]  pages copied.
+ * workspace: bq_kv_pages_workspace bytes, 16-byte aligned, no initial
+ * contents needed; BQ_ERR_WORKSPACE when NULL or smaller.
+ *
+ * kv_fork    row dst[i] becomes a copy of row src[i] (n of each, int32,
+ *            device; dst rows distinct and of length 0): whole pages are
+ *            shared, a partly filled last page is copied.  1 <= n <= rows.
+ * kv_resize  row i gets the length want[i] (int32 [rows], -1: as it is).
+ *            Shorter: pages past it are let go, and a last page that is then
+ *            partly filled and still shared is copied.  Longer: pages are
+ *            taken; their contents are undefined until written.
+ * kv_compact moves pages so that those in use have the lowest ids: the ids in
+ *            use from their number on, ascending, go to the free ids below
+ *            it, ascending; table and refs follow.
+ * kv_copy_pages  copies pages src[i] to dst[i] (int32 [n], device) over all
+ *            layers; pairs outside 0 .. num_pages - 1 are skipped.  No page
+ *            may be both, or twice in dst. */
+int bq_kv_pages_workspace(const bq_kv_cache* cache, int rows, size_t* bytes);
+int bq_kv_fork(const bq_kv_cache* cache, int* table, int* lens, int* refs, int rows, int max_pages, const int* src,
+               const int* dst, int n, int* status, void* workspace, size_t workspace_bytes, void* stream);
+int bq_kv_resize(const bq_kv_cache* cache, int* table, int* lens, int* refs, int rows, int max_pages, const int* want,
+                 int* status, void* workspace, size_t workspace_bytes, void* stream);
+int bq_kv_compact(const bq_kv_cache* cache, int* table, int* refs, int rows, int max_pages, int* status,
+                  void* workspace, size_t workspace_bytes, void* stream);
+int bq_kv_copy_pages(const bq_kv_cache* cache, const int* src, const int* dst, int n, void* stream);
 
 #ifdef __cplusplus
 }

@@ -11,3 +11,5 @@ from .qmv_oracle import (T5_MAX_BYTE, abs_mass, algorithmic_bytes, bits_of, chec
                          t5_pack, t5_unpack, t5_unpack_scalar, tolerance, unpack_words,
                          unpack_words_scalar, weights_f64)
 from .spec_oracle import spec_verify, spec_verify_scalar, target_tokens
+from .kv_oracle import (PagesOracle, kv_append_f64, kv_attn_f64, kv_encode, kv_places, kv_sequence, kv_table,
+                        rope_f64)

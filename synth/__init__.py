@@ -10,3 +10,4 @@ __all__ = [
     "packed_row_bytes", "seed_for", "t5_bytes_per_group",
 ]
 from .spec import QWEN_VOCAB, SpecInputs, make_spec_inputs
+from .kv import make_kv_pool, make_kv_table, rope_freqs
