@@ -14,34 +14,42 @@ const void* rows_kernel(int format) {
   return format == BQ_KV_I8 ? reinterpret_cast<const void*>(&kv_attn_rows_kernel<D, BQ_KV_I8, RT>)
                             : reinterpret_cast<const void*>(&kv_attn_rows_kernel<D, BQ_KV_E4M3, RT>);
 }
-template <int RT>
-const void* pick_rows(int D, int format) {
-  return D == 64 ? rows_kernel<64, RT>(format) : D == 128 ? rows_kernel<128, RT>(format)
-       : D == 192 ? rows_kernel<192, RT>(format) : rows_kernel<256, RT>(format);
+const void* pick_rows(int D, int rows, int format) {
+  if (rows == 32) return D == 64 ? rows_kernel<64, 2>(format) : rows_kernel<128, 2>(format);
+  return D == 64 ? rows_kernel<64, 1>(format) : D == 128 ? rows_kernel<128, 1>(format)
+       : D == 192 ? rows_kernel<192, 1>(format) : rows_kernel<256, 1>(format);
 }
 
+// Workgroups to aim at: one for each CU, whose registers one fills.  Parts
+// beyond that (twice, three times as many) measured slower on every batch:
+// a part costs some 8 us of its own.
+constexpr int kTarget = 256;
+constexpr int kTiles = 4096;  // workgroups from which on no tile is split
 constexpr int kCounters = BQ_KV_ATTN_COUNTER_BYTES / 4;
-constexpr int kTarget = 1024;   // workgroups of a call
-constexpr int kMinPages = 4;    // one page for each wave of a part
 
 // How a call is laid out: rows of a tile, tiles of a head at most, and the
 // workgroups of a head to aim at (0: no tile is split).
 struct Plan {
   int rows;
-  int64_t tiles, target, slot;
+  int64_t tiles, target;
+  size_t bytes;
 };
-Plan plan(const bq_kv_cache* c, int q_heads, int batch, int total, size_t workspace_bytes) {
+Plan plan(const bq_kv_cache* c, int q_heads, int batch, int total, int64_t max_pages, size_t workspace_bytes) {
   Plan p{};
   const int group = q_heads / c->kv_heads;
-  p.rows = 16;
+  // by the rows of a sequence, on average; two row groups of wide heads do
+  // not fit a wave's registers
+  p.rows = (int64_t)total * group > 16 * (int64_t)batch && c->head_dim <= 128 ? 32 : 16;
   p.tiles = std::min(batch, total) + (int64_t)total * group / p.rows;
-  p.slot = (int64_t)kv_part_floats(p.rows, c->head_dim) * 4;
-  // parts that the workspace holds, for each head
-  const int64_t room = workspace_bytes > BQ_KV_ATTN_COUNTER_BYTES
-                           ? ((int64_t)workspace_bytes - BQ_KV_ATTN_COUNTER_BYTES) / (p.slot * c->kv_heads) : 0;
-  const int64_t items = std::min<int64_t>(room, kCounters / c->kv_heads);
-  p.target = std::min<int64_t>(kTarget / c->kv_heads + 1, items - p.tiles);
-  if (p.tiles * c->kv_heads >= kTarget || p.target < 2) p.target = 0;
+  // enough tiles of their own, or more pages than 31 bits count
+  if (p.tiles * c->kv_heads >= kTiles || p.tiles * max_pages > 0x3FFFFFFF) return p;
+  p.target = std::clamp(kTarget / c->kv_heads, 1, kKvMaxParts);
+  // parts that the counters and the workspace hold, for each head
+  const size_t slot = (size_t)kv_part_floats(p.rows, c->head_dim) * 4;
+  const size_t room = workspace_bytes > BQ_KV_ATTN_COUNTER_BYTES ? (workspace_bytes - BQ_KV_ATTN_COUNTER_BYTES) / slot : 0;
+  p.target = std::min<int64_t>(p.target, (int64_t)(std::min(room, (size_t)kCounters) / c->kv_heads) - p.tiles);
+  if (p.target < 2) p.target = 0;
+  if (p.target > 0) p.bytes = BQ_KV_ATTN_COUNTER_BYTES + (size_t)((p.tiles + p.target) * c->kv_heads) * slot;
   return p;
 }
 
@@ -64,8 +72,8 @@ int bq_kv_attn_workspace(const bq_kv_cache* cache, int q_heads, int batch, int t
   *bytes = 0;
   const int st = check_attn(cache, q_heads, batch, total);
   if (st != BQ_OK) return st;
-  const Plan p = plan(cache, q_heads, batch, total, SIZE_MAX / 4);
-  if (p.target > 0) *bytes = BQ_KV_ATTN_COUNTER_BYTES + (size_t)((p.tiles + p.target) * cache->kv_heads * p.slot);
+  const Plan p = plan(cache, q_heads, batch, total, 1, SIZE_MAX);
+  *bytes = p.bytes;
   return BQ_OK;
 }
 
@@ -100,14 +108,20 @@ int bq_kv_attn(const bq_kv_cache* cache, int layer, const void* q, void* out, lo
   p.causal = flags & BQ_KV_CAUSAL;
   p.window = window;
   p.scale = scale * 1.44269504f;
-  const Plan pl = plan(cache, q_heads, batch, total, workspace ? workspace_bytes : 0);
+  const Plan pl = plan(cache, q_heads, batch, total, max_pages, workspace ? workspace_bytes : 0);
   p.target = (int)pl.target;
-  p.min_pages = kMinPages;
   p.counters = static_cast<unsigned*>(workspace);
   p.part = workspace ? reinterpret_cast<float*>(static_cast<char*>(workspace) + BQ_KV_ATTN_COUNTER_BYTES) : nullptr;
-  if (pl.tiles + pl.target > 0x7FFFFFFF) return BQ_ERR_SHAPE;
-  return kv_launch(pick_rows<1>(D, cache->format), dim3((unsigned)(pl.tiles + pl.target), (unsigned)cache->kv_heads),
-                   dim3(256), 0, stream, &p);
+  const int64_t wgs = pl.tiles + pl.target;
+  if (wgs > 0x7FFFFFFF) return BQ_ERR_SHAPE;
+  return kv_launch(pick_rows(D, pl.rows, cache->format), 
+#ifdef XG
+dim3((unsigned)wgs, (unsigned)cache->kv_heads)
+#else
+dim3((unsigned)cache->kv_heads, (unsigned)wgs)
+#endif
+,
+                   dim3((unsigned)(64 * kv_waves(D))), 0, stream, &p);
 }
 
 }  // extern "C"

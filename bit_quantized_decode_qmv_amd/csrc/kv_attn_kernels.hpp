@@ -29,10 +29,9 @@ struct KvAttnParams {
   unsigned* counters;    // workspace: parts done of each tile, zero between calls
   float* part;           // workspace: partial results
   int target;            // workgroups of a head to aim at; 0: tiles are not split
-  int min_pages;         // pages of a part, at least
 };
 
-constexpr int kKvMaxParts = 256;
+constexpr int kKvMaxParts = 128;  // of a tile
 
 __device__ __forceinline__ float kv_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -58,44 +57,97 @@ __device__ __forceinline__ float2 kv_get2(const float* p) {
   return make_float2(__builtin_bit_cast(float, (uint32_t)w), __builtin_bit_cast(float, (uint32_t)(w >> 32)));
 }
 
-// One workgroup's share: a tile of ROWS rows of one sequence, part `split` of
-// `parts` of the pages that the tile sees.
+// One workgroup's share: part `split` of the `parts` of a tile (ROWS rows of
+// one sequence); the parts of a tile are `chunk` pages each, the last one
+// what is left.  The list of a head's shares has the whole parts of all tiles
+// first and their last parts after them, so that no workgroup begins a long
+// part when others are done.
 struct KvWork {
-  int b, tile, split, parts;
+  KvSeq s;
+  int b, tile, split, parts, chunk;
+  int slot;  // place of the tile's part 0 when the parts are kept tile by tile
 };
 __device__ __forceinline__ int kv_first_page(const KvAttnParams& p, const KvSeq& s) {
   return p.causal && p.window > 0 ? max(s.len - s.n - p.window + 1, 0) / kKvPage : 0;
 }
+// Every wave of the grid finds its share from the batch's arrays: a lane
+// takes a sequence (64 at a time; the first 64 stay in its registers).
 template <int ROWS>
 __device__ __forceinline__ bool kv_attn_work(const KvAttnParams& p, int item, KvWork& w) {
+  const int lane = (int)threadIdx.x & 63, batch = p.batch.batch;
   const auto pages = [&](const KvSeq& s) {
     return max((s.len + kKvPage - 1) / kKvPage - kv_first_page(p, s), 1);
   };
   const auto tiles = [&](const KvSeq& s) { return (s.n * p.group + ROWS - 1) / ROWS; };
-  int chunk = 0x7FFFFFFF;
-  if (p.target > 0) {
-    // pages of a part: the batch's tiles times pages over the target, so a
-    // long sequence gets as many more parts as it has more pages
-    long long all = 0;
-    for (int i = (int)(threadIdx.x & 63); i < p.batch.batch; i += 64) {
-      const KvSeq s = kv_seq(p.batch, i);
-      all += (long long)tiles(s) * pages(s);
-    }
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) all += __shfl_xor(all, o, 64);
-    chunk = (int)min(max((all + p.target - 1) / p.target, (long long)p.min_pages), (long long)0x7FFFFFFF);
-  }
-  const auto parts = [&](const KvSeq& s) {
-    return p.target > 0 ? min((pages(s) + chunk - 1) / chunk, kKvMaxParts) : 1;
+  const KvSeq first = lane < batch ? kv_seq(p.batch, lane) : KvSeq{};
+  const auto seq = [&](int base) {
+    return base == 0 ? first : base + lane < batch ? kv_seq(p.batch, base + lane) : KvSeq{};
   };
-  int local;
-  if (!kv_locate(item, p.batch.batch, [&](int i) { const KvSeq s = kv_seq(p.batch, i); return tiles(s) * parts(s); },
-                 w.b, local))
-    return false;
-  w.parts = __builtin_amdgcn_readfirstlane(parts(kv_seq(p.batch, w.b)));
-  w.tile = local / w.parts;
-  w.split = local - w.tile * w.parts;
-  return true;
+  w.chunk = 0x7FFFFFFF;
+  if (p.target > 0) {
+    // the batch's tiles times pages over the target: a long sequence gets as
+    // many more parts as it has more pages
+    int all = 0;
+    for (int base = 0; base < batch; base += 64) all += tiles(seq(base)) * pages(seq(base));
+    all = __builtin_amdgcn_readlane(kv_scan(all), 63);
+    // no part shorter than pays for joining it (measured, one sequence, 8
+    // heads of 128: 16 pages 10.0 us in one part and 11.9 in two; 32 pages
+    // 14.4 us in parts of 16 and 11.9 in parts of 8; 2047 pages of one head
+    // 28.6 us in parts of 16 and 41.1 in parts of 8)
+    const int least = all <= 16 || all > 64 ? 16 : 8;
+    w.chunk = max((int)(((unsigned)all + p.target - 1) / (unsigned)p.target), least);
+  }
+  // whole parts ahead of a tile's last one
+  const auto whole = [&](const KvSeq& s) { return (int)((unsigned)(pages(s) - 1) / (unsigned)w.chunk); };
+  // sequence `at` of the 64 from `base`, its tile's part 0 after `before` others
+  const auto take = [&](int base, int at, int before) {
+    const KvSeq s = seq(base);
+    w.b = base + at;
+    w.s.q0 = __builtin_amdgcn_readlane(s.q0, at);
+    w.s.n = __builtin_amdgcn_readlane(s.n, at);
+    w.s.len = __builtin_amdgcn_readlane(s.len, at);
+    w.parts = (p.target > 0 ? __builtin_amdgcn_readlane(whole(s), at) : 0) + 1;
+    w.slot = before + w.tile * w.parts;
+  };
+  int wholes = 0;
+  if (p.target > 0) {
+    int before_tiles = 0;
+    for (int base = 0; base < batch; base += 64) {
+      const KvSeq s = seq(base);
+      const int nt = tiles(s), nw = nt * whole(s);
+      const int st = kv_scan(nt), sw = kv_scan(nw);
+      const int all_w = __builtin_amdgcn_readlane(sw, 63);
+      if (item < wholes + all_w) {
+        const int at = __builtin_ctzll(__ballot(wholes + sw > item));
+        const int from = wholes + __builtin_amdgcn_readlane(sw - nw, at);
+        const int each = __builtin_amdgcn_readlane(whole(s), at);
+        w.tile = (int)((unsigned)(item - from) / (unsigned)each);
+        w.split = item - from - w.tile * each;
+        take(base, at, from + before_tiles + __builtin_amdgcn_readlane(st - nt, at));
+        return true;
+      }
+      wholes += all_w;
+      before_tiles += __builtin_amdgcn_readlane(st, 63);
+    }
+  }
+  int before_tiles = 0, before_wholes = 0;
+  for (int base = 0; base < batch; base += 64) {
+    const KvSeq s = seq(base);
+    const int nt = tiles(s), nw = p.target > 0 ? nt * whole(s) : 0;
+    const int st = kv_scan(nt), sw = p.target > 0 ? kv_scan(nw) : 0;
+    const int mine = item - wholes - before_tiles, all_t = __builtin_amdgcn_readlane(st, 63);
+    if (mine < all_t) {
+      const int at = __builtin_ctzll(__ballot(st > mine));
+      const int from = __builtin_amdgcn_readlane(st - nt, at);
+      w.tile = mine - from;
+      take(base, at, before_tiles + from + before_wholes + __builtin_amdgcn_readlane(sw - nw, at));
+      w.split = w.parts - 1;
+      return true;
+    }
+    before_tiles += all_t;
+    before_wholes += __builtin_amdgcn_readlane(sw, 63);
+  }
+  return false;
 }
 
 // Rows 16t + l % 16 of a tile: the tokens each sees are [lo, hi).
@@ -110,28 +162,83 @@ __device__ __forceinline__ KvRowRange kv_row_range(const KvAttnParams& p, const 
   return r;
 }
 
-// Floats of a part's partial result: (max, sum) of each row, then O [ROWS][D].
+// Floats of a part's result: (max, sum) of each row, then O [ROWS][D].
 __host__ __device__ constexpr int kv_part_floats(int rows, int D) { return rows * (D + 2); }
 
-// Few rows: four waves share a part's pages (every fourth), each with its own
-// running maximum and sum; they are joined through LDS, and the parts of a
-// tile by the workgroup that finishes last.
+// Buffer descriptor over the codes of one head's page; bytes 0: every load
+// gives zeros and touches no memory.
+typedef __amdgpu_buffer_rsrc_t kv_rsrc_t;
+__device__ __forceinline__ kv_rsrc_t kv_rsrc(const void* base, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, bytes, 0x00020000);
+}
+
+// One page's codes in flight or at hand, as a wave holds them.
+template <int D>
+struct KvCodes {
+  u32x4_t k[4][D / 64], v[D / 16];
+};
+
+// Waves of a workgroup: two for each SIMD as long as their registers allow.
+constexpr int kv_waves(int D) { return D <= 128 ? 8 : 4; }
+
+// Few rows: a workgroup's waves share a part's pages in turn, each with its
+// own running maximum and sum; they are joined through LDS, and the parts of
+// a tile by the workgroup that finishes last.
+//
+// Bound by HBM (each code is read once).  A wave's registers hold one page:
+// the next page's K is requested as soon as the scores are formed, its V as
+// soon as the outputs are, so a wave always has a page's worth of loads in
+// flight while it computes.  Every load is issued (past the last page from an
+// empty descriptor): a conditional load would make the compiler wait for all
+// that are in flight.
+//
+// The running maximum is raised only when a score passes it by more than 8
+// (in log2): then the four lanes of a column agree on a new one and the
+// outputs are rescaled.  Otherwise a page costs no step across lanes, and the
+// probabilities, at most 2^8, stay well inside fp16.  They are taken as the
+// sum of two fp16 numbers, so that no more than 2^-22 of a probability is
+// lost: the second product is cheap beside the loads.
 template <int D, int FMT, int RT>
-__global__ __launch_bounds__(256) void kv_attn_rows_kernel(KvAttnParams p) {
-  constexpr int C = D / 64, N = D / 16, ROWS = 16 * RT;
-  __shared__ __align__(16) float lds[2 * 64 * RT * (4 * N + 2) > 2 * kKvMaxParts * ROWS ? 2 * 64 * RT * (4 * N + 2)
-                                                                                     : 2 * kKvMaxParts * ROWS];
+__global__ __launch_bounds__(64 * kv_waves(D)) void kv_attn_rows_kernel(KvAttnParams p) {
+  constexpr int C = D / 64, N = D / 16, ROWS = 16 * RT, NW = kv_waves(D), THREADS = 64 * NW;
+  constexpr int JOIN = NW * (N * 256 + 32);
+  __shared__ __align__(16) float lds[JOIN > 2 * kKvMaxParts * ROWS ? JOIN : 2 * kKvMaxParts * ROWS];
   __shared__ int last;
-  const int lane = (int)threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int item = (int)blockIdx.x, head = (int)blockIdx.y;
+  const int lane = (int)threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  const int item = (int)blockIdx.y, head = (int)blockIdx.x;
   KvWork w;
   if (!kv_attn_work<ROWS>(p, item, w)) return;
-  KvSeq s = kv_seq(p.batch, w.b);
-  s.q0 = __builtin_amdgcn_readfirstlane(s.q0);
-  s.n = __builtin_amdgcn_readfirstlane(s.n);
-  s.len = __builtin_amdgcn_readfirstlane(s.len);
+  const KvSeq s = w.s;
   const int rows = s.n * p.group, row0 = w.tile * ROWS;
+
+  // the tile's pages, and the tokens that all its rows see
+  const int tok0 = row0 / p.group, tok1 = min((row0 + ROWS - 1) / p.group, s.n - 1);
+  const KvRowRange r0 = kv_row_range(p, s, tok0), r1 = kv_row_range(p, s, tok1);
+  const int pa = r0.lo / kKvPage, pages = max((r1.hi + kKvPage - 1) / kKvPage - pa, 0);
+  const int begin = pa + (w.parts > 1 ? w.split * w.chunk : 0);
+  const int end = pa + (w.split == w.parts - 1 ? pages : min((w.split + 1) * w.chunk, pages));
+
+  // requests of a page: its place in the cache, or none
+  const auto place = [&](int at) -> int64_t {
+    const int page = at < end ? kv_page(p.batch, w.b, at) : -1;
+    return page < 0 ? -1 : (int64_t)page * p.kv_heads + head;
+  };
+  KvCodes<D> x;
+  const auto load_k = [&](int64_t at) {
+    const kv_rsrc_t rs = kv_rsrc(p.k + max(at, (int64_t)0) * (kKvPage * D), at < 0 ? 0 : kKvPage * D);
+#pragma unroll
+    for (int i = 0; i < 4 * C; ++i)
+      x.k[i / C][i % C] = __builtin_amdgcn_raw_buffer_load_b128(rs, lane * 16, i * 1024, 0);
+  };
+  const auto load_v = [&](int64_t at) {
+    const kv_rsrc_t rs = kv_rsrc(p.v + max(at, (int64_t)0) * (kKvPage * D), at < 0 ? 0 : kKvPage * D);
+#pragma unroll
+    for (int n = 0; n < N; ++n) x.v[n] = __builtin_amdgcn_raw_buffer_load_b128(rs, lane * 16, n * 1024, 0);
+  };
+  int64_t here = place(begin + wave);
+  load_k(here);
+  load_v(here);
 
   // Q as the B operand: column r, k = dims 64c + 16g + 8h .. + 7
   half8_t q[RT][2 * C];
@@ -149,12 +256,6 @@ __global__ __launch_bounds__(256) void kv_attn_rows_kernel(KvAttnParams p) {
     for (int c = 0; c < 2 * C; ++c)
       q[t][c] = ok ? *reinterpret_cast<const half8_t*>(src + (c >> 1) * 64 + (c & 1) * 8) : half8_t{};
   }
-  // the tile's pages, and the tokens that all its rows see
-  const int tok0 = row0 / p.group, tok1 = min((row0 + ROWS - 1) / p.group, s.n - 1);
-  const KvRowRange r0 = kv_row_range(p, s, tok0), r1 = kv_row_range(p, s, tok1);
-  const int pa = r0.lo / kKvPage, pages = max((r1.hi + kKvPage - 1) / kKvPage - pa, 0);
-  const int begin = pa + (int)((int64_t)pages * w.split / w.parts);
-  const int end = pa + (int)((int64_t)pages * (w.split + 1) / w.parts);
 
   f32x4 o[RT][N];
   float m[RT], l[RT];
@@ -167,209 +268,222 @@ __global__ __launch_bounds__(256) void kv_attn_rows_kernel(KvAttnParams p) {
     for (int n = 0; n < N; ++n) o[t][n] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
 
-  for (int at = begin + wave; at < end; at += 4) {
-    const int page = kv_page(p.batch, w.b, at);
-    if (page < 0) continue;
-    const int64_t head_at = (int64_t)page * p.kv_heads + head;
-    const u32x4_t* kp = reinterpret_cast<const u32x4_t*>(p.k + head_at * (kKvPage * D)) + lane;
-    const u32x4_t* vp = reinterpret_cast<const u32x4_t*>(p.v + head_at * (kKvPage * D)) + lane;
-    u32x4_t kr[4][C], vr[N];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int c = 0; c < C; ++c) kr[i][c] = kp[(i * C + c) * 64];
-#pragma unroll
-    for (int n = 0; n < N; ++n) vr[n] = vp[n * 64];
-    float sk[4], sv[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      sk[i] = p.ks[head_at * kKvBlocks + i];
-      sv[i] = p.vs[head_at * kKvBlocks + i];
-    }
-    const int j0 = at * kKvPage, left = s.len - j0;  // tokens of the page that are held
-    if (left < kKvPage) {
-      // what lies past the length is never used: neither a scale nor, in
-      // e4m3, a code that is no number
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (16 * i >= left) sv[i] = 0.f;
-        if constexpr (FMT == BQ_KV_E4M3) {
-          const int keep = min(max(left - 16 * i - 4 * g, 0), 4);
-          const uint32_t mask = keep == 4 ? 0xFFFFFFFFu : (1u << (8 * keep)) - 1u;
-#pragma unroll
-          for (int n = 0; n < N; ++n) vr[n][i] &= mask;
-        }
-      }
-    }
+  for (int at = begin + wave; at < end; at += NW) {
+    const int64_t next = place(at + NW);
+    const int64_t ph = max(here, (int64_t)0);
+    const f32x4 skv = *reinterpret_cast<const f32x4*>(p.ks + ph * kKvBlocks);
+    f32x4 sv = *reinterpret_cast<const f32x4*>(p.vs + ph * kKvBlocks);
+    const int j0 = at * kKvPage;
+    const int left = here < 0 ? 0 : s.len - j0;  // tokens of the page that are held
 
     // scores, in units of log2
-    f32x4 x[RT][4];
+    f32x4 y[RT][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
 #pragma unroll
-      for (int t = 0; t < RT; ++t) x[t][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int t = 0; t < RT; ++t) y[t][i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const half8_t a0 = kv_half8<FMT>(kr[i][c][0], kr[i][c][1]), a1 = kv_half8<FMT>(kr[i][c][2], kr[i][c][3]);
+        const half8_t a0 = kv_half8<FMT>(x.k[i][c][0], x.k[i][c][1]), a1 = kv_half8<FMT>(x.k[i][c][2], x.k[i][c][3]);
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
-          x[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a0, q[t][2 * c], x[t][i], 0, 0, 0);
-          x[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a1, q[t][2 * c + 1], x[t][i], 0, 0, 0);
+          y[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a0, q[t][2 * c], y[t][i], 0, 0, 0);
+          y[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a1, q[t][2 * c + 1], y[t][i], 0, 0, 0);
         }
       }
+    }
+    load_k(next);
 #pragma unroll
-      for (int t = 0; t < RT; ++t)
+    for (int t = 0; t < RT; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int j = j0 + 16 * i + 4 * g + e;
-          const float y = x[t][i][e] * (sk[i] * p.scale);
-          x[t][i][e] = j >= lo[t] && j < hi[t] ? y : -__builtin_inff();
+      for (int i = 0; i < 4; ++i) y[t][i] *= skv[i] * p.scale;
+    if (left < kKvPage || j0 + kKvPage > r0.hi || j0 < r1.lo) {
+      // a page that some row does not see whole: the row's tokens [lo, hi)
+      // as one unsigned comparison of each token
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        const int from = max(lo[t] - j0, 0), count = max(min(hi[t] - j0, left) - from, 0);
+        int in = 4 * g - from;
+        // stays in this branch: computed ahead of it, it would cost every page
+        asm volatile("" : "+v"(in));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            y[t][i][e] = (unsigned)(in + 16 * i + e) < (unsigned)count ? y[t][i][e] : -__builtin_inff();
+      }
+      // what lies past the length is never used: neither a scale nor, in
+      // e4m3, a code that is no number
+      if (left < kKvPage) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (16 * i >= left) sv[i] = 0.f;
+          if constexpr (FMT == BQ_KV_E4M3) {
+            const int keep = min(max(left - 16 * i - 4 * g, 0), 4);
+            const uint32_t mask = keep == 4 ? 0xFFFFFFFFu : (1u << (8 * keep)) - 1u;
+#pragma unroll
+            for (int n = 0; n < N; ++n) x.v[n][i] &= mask;
+          }
         }
+      }
     }
 
     // running maximum and units of o
     const float rmax = __builtin_fmaxf(__builtin_fmaxf(sv[0], sv[1]), __builtin_fmaxf(sv[2], sv[3]));
-    float change = 1.f;
-    if (rmax > R) {
-      float up = R;
-      const int ex = (int)((__builtin_bit_cast(uint32_t, rmax) >> 23) & 255u) + 1;  // the power of two above rmax
-      up = __builtin_bit_cast(float, (uint32_t)min(ex, 253) << 23);
-      change = R / up;
-      R = up;
-      invR = 1.f / up;
-    }
-    half8_t pb[RT][2];
+    float mx[RT];
+    bool raise = rmax > R;
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-      float mx = -__builtin_inff();
+      mx[t] = y[t][0][0];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) mx = __builtin_fmaxf(mx, x[t][i][e]);
-      const float mn = __builtin_fmaxf(m[t], kv_col_max(mx));
-      const float base = mn == -__builtin_inff() ? 0.f : mn;  // a row that has seen nothing yet
-      const float alpha = kv_exp2(m[t] - base);
-      m[t] = mn;
-      float sum = 0.f;
+        for (int e = 0; e < 4; ++e) mx[t] = __builtin_fmaxf(mx[t], y[t][i][e]);
+      raise = raise || mx[t] > m[t] + 8.f;
+    }
+    if (__ballot(raise) != 0) {
+      float change = 1.f;
+      if (rmax > R) {
+        // the power of two above the largest scale
+        const int ex = (int)((__builtin_bit_cast(uint32_t, rmax) >> 23) & 255u) + 1;
+        const float up = __builtin_bit_cast(float, (uint32_t)min(ex, 253) << 23);
+        change = R / up;
+        R = up;
+        invR = 1.f / up;
+      }
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        const float mn = __builtin_fmaxf(m[t], kv_col_max(mx[t]));
+        const float alpha = mn == -__builtin_inff() ? 1.f : kv_exp2(m[t] - mn);
+        m[t] = mn;
+        l[t] *= alpha;
+#pragma unroll
+        for (int n = 0; n < N; ++n) o[t][n] *= alpha * change;
+      }
+    }
+    half8_t ph_[RT][2], pl_[RT][2];
+    const f32x4 unit = sv * invR;
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      const float base = m[t] == -__builtin_inff() ? 0.f : m[t];  // a row that has seen nothing yet
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float e2 = kv_exp2(x[t][i][e] - base);
-          sum += e2;
-          pb[t][i >> 1][(i & 1) * 4 + e] = (_Float16)(e2 * (sv[i] * invR));
+          const float e2 = kv_exp2(y[t][i][e] - base);
+          l[t] += e2;
+          const float f = e2 * unit[i];
+          const _Float16 h = (_Float16)f;
+          ph_[t][i >> 1][(i & 1) * 4 + e] = h;
+          pl_[t][i >> 1][(i & 1) * 4 + e] = (_Float16)(f - (float)h);
         }
-      l[t] = l[t] * alpha + sum;
-#pragma unroll
-      for (int n = 0; n < N; ++n) o[t][n] *= alpha * change;
     }
 #pragma unroll
     for (int n = 0; n < N; ++n)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const half8_t a = kv_half8<FMT>(vr[n][2 * h], vr[n][2 * h + 1]);
+        const half8_t a = kv_half8<FMT>(x.v[n][2 * h], x.v[n][2 * h + 1]);
 #pragma unroll
-        for (int t = 0; t < RT; ++t) o[t][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pb[t][h], o[t][n], 0, 0, 0);
-      }
-  }
-
-  // o in its own units, the sum over a column's four lanes
-#pragma unroll
-  for (int t = 0; t < RT; ++t) {
-    l[t] = kv_col_sum(l[t]);
-#pragma unroll
-    for (int n = 0; n < N; ++n) o[t][n] *= R;
-  }
-  // waves 2, 3 into 0, 1, then 1 into 0
-#pragma unroll
-  for (int step = 2; step >= 1; step >>= 1) {
-    float* box = lds + (wave & (step - 1)) * (64 * RT * (4 * N + 2));
-    if (wave >= step && wave < 2 * step) {
-#pragma unroll
-      for (int t = 0; t < RT; ++t) {
-#pragma unroll
-        for (int n = 0; n < N; ++n) *reinterpret_cast<f32x4*>(box + ((t * N + n) * 64 + lane) * 4) = o[t][n];
-        box[(RT * N * 4 + 2 * t) * 64 + lane] = m[t];
-        box[(RT * N * 4 + 2 * t + 1) * 64 + lane] = l[t];
-      }
-    }
-    __syncthreads();
-    if (wave < step) {
-#pragma unroll
-      for (int t = 0; t < RT; ++t) {
-        const float m2 = box[(RT * N * 4 + 2 * t) * 64 + lane], l2 = box[(RT * N * 4 + 2 * t + 1) * 64 + lane];
-        const float mn = __builtin_fmaxf(m[t], m2), base = mn == -__builtin_inff() ? 0.f : mn;
-        const float a1 = kv_exp2(m[t] - base), a2 = kv_exp2(m2 - base);
-        m[t] = mn;
-        l[t] = l[t] * a1 + l2 * a2;
-#pragma unroll
-        for (int n = 0; n < N; ++n)
-          o[t][n] = o[t][n] * a1 + *reinterpret_cast<const f32x4*>(box + ((t * N + n) * 64 + lane) * 4) * a2;
-      }
-    }
-    __syncthreads();
-  }
-
-  if (w.parts == 1) {
-    if (wave == 0) {
-#pragma unroll
-      for (int t = 0; t < RT; ++t) {
-        const int row = row0 + 16 * t + r;
-        if (row >= rows) continue;
-        const int token = row / p.group, qh = head * p.group + row - token * p.group;
-        const float inv = l[t] > 0.f ? 1.f / l[t] : 0.f;  // nothing seen: zeros
-        _Float16* dst = p.out + (int64_t)(s.q0 + token) * p.out_stride + qh * D + 4 * g;
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-          const f32x4 y = o[t][n] * inv;
-          *reinterpret_cast<half4_t*>(dst + 16 * n) =
-              half4_t{(_Float16)y[0], (_Float16)y[1], (_Float16)y[2], (_Float16)y[3]};
+        for (int t = 0; t < RT; ++t) {
+          o[t][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, ph_[t][h], o[t][n], 0, 0, 0);
+          o[t][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pl_[t][h], o[t][n], 0, 0, 0);
         }
       }
-    }
-    return;
+    load_v(next);
+    here = next;
   }
 
-  // The part's result goes to its slot; the workgroup that counts last joins
-  // the tile's parts, in order (the same result on every call).
+  // The waves' results are joined through LDS, 16 rows at a time: a thread
+  // adds up four values of a row.
   constexpr int SLOT = kv_part_floats(ROWS, D);
-  float* tile_part = p.part + ((int64_t)(item - w.split) * p.kv_heads + head) * SLOT;
-  const int64_t next = (int64_t)p.kv_heads * SLOT;
-  unsigned* counter = p.counters + (int64_t)(item - w.split) * p.kv_heads + head;
-  if (wave == 0) {
-    float* mine = tile_part + w.split * next;
+  const auto slot = [&](int part) { return p.part + ((int64_t)(w.slot + part) * p.kv_heads + head) * SLOT; };
+  float *ml = lds + NW * N * 256;  // [wave][16 rows] (max, sum)
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
-      const int row = 16 * t + r;
-      if (row0 + row >= rows) continue;
-      if (g == 0) kv_put2(mine + 2 * row, m[t], l[t]);
-      float* dst = mine + 2 * ROWS + row * D + 4 * g;
+  for (int t = 0; t < RT; ++t) {
+    const float sum = kv_col_sum(l[t]);
 #pragma unroll
-      for (int n = 0; n < N; ++n) {
-        kv_put2(dst + 16 * n, o[t][n][0], o[t][n][1]);
-        kv_put2(dst + 16 * n + 2, o[t][n][2], o[t][n][3]);
-      }
+    for (int n = 0; n < N; ++n) *reinterpret_cast<f32x4*>(lds + ((wave * N + n) * 64 + lane) * 4) = o[t][n] * R;
+    if (g == 0) *reinterpret_cast<float2*>(ml + (wave * 16 + r) * 2) = make_float2(m[t], sum);
+    __syncthreads();
+    const int row = 16 * t + r;  // of the tile; the same for all that a thread takes
+    float2 of[NW];
+    float mx = -__builtin_inff(), all = 0.f;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      of[i] = *reinterpret_cast<const float2*>(ml + (i * 16 + r) * 2);
+      mx = __builtin_fmaxf(mx, of[i].x);
     }
-    // the stores are performed at device scope before the count is
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    if (lane == 0)
-      last = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (unsigned)(w.parts - 1);
+    const float base = mx == -__builtin_inff() ? 0.f : mx;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      of[i].x = kv_exp2(of[i].x - base);
+      all += of[i].y * of[i].x;
+    }
+    if (row0 + row < rows) {
+      const int token = (row0 + row) / p.group, qh = head * p.group + row0 + row - token * p.group;
+      _Float16* dst = p.out + (int64_t)(s.q0 + token) * p.out_stride + qh * D + 4 * g;
+      float* mine = slot(w.split);
+      const float inv = all > 0.f ? 1.f / all : 0.f;  // nothing seen: zeros
+#pragma unroll
+      for (int n = wave; n < N; n += NW) {
+        f32x4 y = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < NW; ++i) y += *reinterpret_cast<const f32x4*>(lds + ((i * N + n) * 64 + lane) * 4) * of[i].x;
+        if (w.parts == 1) {
+          y *= inv;
+          *reinterpret_cast<half4_t*>(dst + 16 * n) =
+              half4_t{(_Float16)y[0], (_Float16)y[1], (_Float16)y[2], (_Float16)y[3]};
+        } else {
+          float* to = mine + 2 * ROWS + row * D + 16 * n + 4 * g;
+          kv_put2(to, y[0], y[1]);
+          kv_put2(to + 2, y[2], y[3]);
+        }
+      }
+      if (w.parts > 1 && wave == 0 && g == 0) kv_put2(mine + 2 * row, mx, all);
+    }
+    if (t + 1 < RT) __syncthreads();
   }
+  if (w.parts == 1) return;
+
+  // The part's result is in its slot; the workgroup that counts last joins
+  // the tile's parts, in order (the same result on every call).
+  unsigned* counter = p.counters + (int64_t)w.slot * p.kv_heads + head;
+  // every wave's stores are performed at device scope before the count is
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  if (threadIdx.x == 0)
+    last = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (unsigned)(w.parts - 1);
   __syncthreads();
   if (!last) return;
-  const int some = min(ROWS, rows - row0);
+  // Two values of the tile a thread, or, where the tile has fewer, a share of
+  // the parts of two values; AHEAD parts are requested at a time, the first
+  // of them together with the maxima and sums.
+  constexpr int AHEAD = 16;
+  const int some = min(ROWS, rows - row0), pairs = some * (D / 2);
+  const int groups = max(THREADS / pairs, 1);
+  const int tid = (int)threadIdx.x, group = groups > 1 ? tid / pairs : 0;
   float *wm = lds, *wl = lds + kKvMaxParts * ROWS;
-  for (int i = (int)threadIdx.x; i < w.parts * ROWS; i += 256) {
+  float2 v[AHEAD];
+  const auto request = [&](int at, int k0) {
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      const int part = min(group + (k0 + k) * groups, w.parts - 1);
+      v[k] = kv_get2(slot(part) + 2 * ROWS + 2 * min(at, pairs - 1));  // no branch: all are in flight at once
+    }
+  };
+  int at = groups > 1 ? (group < groups ? tid - group * pairs : pairs) : tid;
+  request(at, 0);
+  for (int i = tid; i < w.parts * ROWS; i += THREADS) {
     const int part = i / ROWS, row = i % ROWS;
     float2 ml = make_float2(-__builtin_inff(), 0.f);
-    if (row < some) ml = kv_get2(tile_part + part * next + 2 * row);
+    if (row < some) ml = kv_get2(slot(part) + 2 * row);
     wm[i] = ml.x;
     wl[i] = ml.y;
   }
   __syncthreads();
   {
-    constexpr int PER = 256 / ROWS;  // consecutive lanes of a row
-    const int row = (int)threadIdx.x / PER, sub = (int)threadIdx.x % PER;
+    constexpr int PER = THREADS / ROWS;  // consecutive lanes of a row
+    const int row = tid / PER, sub = tid % PER;
     float mx = -__builtin_inff(), sum = 0.f;
     for (int i = sub; i < w.parts; i += PER) mx = __builtin_fmaxf(mx, wm[i * ROWS + row]);
 #pragma unroll
@@ -382,19 +496,36 @@ __global__ __launch_bounds__(256) void kv_attn_rows_kernel(KvAttnParams p) {
     for (int i = sub; i < w.parts; i += PER) wm[i * ROWS + row] = kv_exp2(wm[i * ROWS + row] - base) * inv;
   }
   __syncthreads();
-  for (int i = (int)threadIdx.x; i < some * (D / 2); i += 256) {
-    const int row = i / (D / 2), d2 = i % (D / 2);
-    float a = 0.f, b = 0.f;
-#pragma unroll 8
-    for (int part = 0; part < w.parts; ++part) {
-      const float2 v = kv_get2(tile_part + part * next + 2 * ROWS + row * D + 2 * d2);
-      const float f = wm[part * ROWS + row];
-      a += v.x * f;
-      b += v.y * f;
+  for (bool fresh = true; __syncthreads_or(at < pairs); at += THREADS, fresh = false) {
+    const int row = min(at, pairs - 1) / (D / 2);
+    float2 sum = make_float2(0.f, 0.f);
+    if (!fresh) request(at, 0);
+    for (int k0 = 0; k0 * groups < w.parts; k0 += AHEAD) {
+      if (k0 > 0) request(at, k0);
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) {
+        const int part = group + (k0 + k) * groups;
+        const float f = part < w.parts ? wm[part * ROWS + row] : 0.f;
+        sum.x += v[k].x * f;
+        sum.y += v[k].y * f;
+      }
     }
-    const int token = (row0 + row) / p.group, qh = head * p.group + row0 + row - token * p.group;
-    *reinterpret_cast<half2_t*>(p.out + (int64_t)(s.q0 + token) * p.out_stride + qh * D + 2 * d2) =
-        half2_t{(_Float16)a, (_Float16)b};
+    if (groups > 1) {
+      if (at < pairs) reinterpret_cast<float2*>(wl)[group * pairs + at] = sum;
+      __syncthreads();
+      if (group == 0 && at < pairs)
+        for (int i = 1; i < groups; ++i) {
+          const float2 other = reinterpret_cast<const float2*>(wl)[i * pairs + at];
+          sum.x += other.x;
+          sum.y += other.y;
+        }
+    }
+    if (group == 0 && at < pairs) {
+      const int token = (row0 + row) / p.group, qh = head * p.group + row0 + row - token * p.group;
+      *reinterpret_cast<half2_t*>(p.out + (int64_t)(s.q0 + token) * p.out_stride + qh * D + 2 * (at % (D / 2))) =
+          half2_t{(_Float16)sum.x, (_Float16)sum.y};
+    }
+    if (groups > 1) break;
   }
   if (threadIdx.x == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }

@@ -142,6 +142,18 @@ __device__ __forceinline__ int kv_touched(const KvSeq& s, int& first) {
   return s.n > 0 && s.len > 0 ? (s.len - 1) / kKvPage - first + 1 : 0;
 }
 
+// Inclusive prefix sums over a wave's lanes, in six adds of lanes nearby (data
+// parallel primitives: shifts within rows of 16, then broadcasts across rows).
+__device__ __forceinline__ int kv_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast:15 into rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast:31 into rows 2 and 3
+  return v;
+}
+
 // Item `item` of a list in which sequence b has count(b) items: the sequence
 // and the item's place among its own.  Called by whole waves; every lane gets
 // the same (scalar) answer; false past the list's end.
@@ -150,12 +162,7 @@ __device__ __forceinline__ bool kv_locate(int item, int batch, Count count, int&
   const int lane = threadIdx.x & 63;
   for (int base = 0; base < batch; base += 64) {
     const int c = base + lane < batch ? count(base + lane) : 0;
-    int s = c;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int t = __shfl_up(s, o, 64);
-      if (lane >= o) s += t;
-    }
+    const int s = kv_scan(c);
     const int all = __builtin_amdgcn_readlane(s, 63);
     if (item < all) {
       const int at = __builtin_ctzll(__ballot(s > item));
