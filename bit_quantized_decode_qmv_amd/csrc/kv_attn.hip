@@ -3,7 +3,7 @@
 #include <algorithm>
 #include <cmath>
 
-#include "kv_attn_kernels.hpp"
+#include "kv_prompt_kernels.hpp"
 
 namespace {
 
@@ -20,11 +20,30 @@ const void* pick_rows(int D, int rows, int format) {
        : D == 192 ? rows_kernel<192, 1>(format) : rows_kernel<256, 1>(format);
 }
 
-// Workgroups to aim at: one for each CU, whose registers one fills.  Parts
-// beyond that (twice, three times as many) measured slower on every batch:
-// a part costs some 8 us of its own.
-constexpr int kTarget = 256;
-constexpr int kTiles = 4096;  // workgroups from which on no tile is split
+template <int D>
+const void* prompt_kernel(int format) {
+  return format == BQ_KV_I8 ? reinterpret_cast<const void*>(&kv_attn_prompt_kernel<D, BQ_KV_I8>)
+                            : reinterpret_cast<const void*>(&kv_attn_prompt_kernel<D, BQ_KV_E4M3>);
+}
+const void* pick_prompt(int D, int format) {
+  return D == 64 ? prompt_kernel<64>(format) : D == 128 ? prompt_kernel<128>(format)
+       : D == 192 ? prompt_kernel<192>(format) : prompt_kernel<256>(format);
+}
+const void* pick_join(int D) {
+  return D == 64 ? reinterpret_cast<const void*>(&kv_attn_join_kernel<64>)
+       : D == 128 ? reinterpret_cast<const void*>(&kv_attn_join_kernel<128>)
+       : D == 192 ? reinterpret_cast<const void*>(&kv_attn_join_kernel<192>)
+                  : reinterpret_cast<const void*>(&kv_attn_join_kernel<256>);
+}
+
+#ifndef XP
+#define XP 32
+#endif
+// Few rows: workgroups to aim at, one for each CU, whose registers one fills.
+// Parts beyond that (twice, three times as many) measured slower on every
+// batch: a part costs some 8 us of its own.  From kRowTiles workgroups on no
+// tile is split.
+constexpr int kTarget = 256, kRowTiles = 4096;
 constexpr int kCounters = BQ_KV_ATTN_COUNTER_BYTES / 4;
 
 // How a call is laid out: rows of a tile, tiles of a head at most, and the
@@ -36,18 +55,22 @@ struct Plan {
 };
 Plan plan(const bq_kv_cache* c, int q_heads, int batch, int total, int64_t max_pages, size_t workspace_bytes) {
   Plan p{};
-  const int group = q_heads / c->kv_heads;
   // by the rows of a sequence, on average; two row groups of wide heads do
   // not fit a wave's registers
-  p.rows = (int64_t)total * group > 16 * (int64_t)batch && c->head_dim <= 128 ? 32 : 16;
-  p.tiles = std::min(batch, total) + (int64_t)total * group / p.rows;
+  const int64_t rows = (int64_t)total * (q_heads / c->kv_heads);
+  const bool narrow = c->head_dim <= 128;
+  p.rows = rows <= 16 * (int64_t)batch ? 16 : narrow && rows <= XP * (int64_t)batch ? 32 : kPromptRows;
+  p.tiles = std::min(batch, total) + rows / p.rows;
+  const bool prompt = p.rows == kPromptRows;
+  const int wgs = prompt && narrow ? 2 * kTarget : kTarget;
   // enough tiles of their own, or more pages than 31 bits count
-  if (p.tiles * c->kv_heads >= kTiles || p.tiles * max_pages > 0x3FFFFFFF) return p;
-  p.target = std::clamp(kTarget / c->kv_heads, 1, kKvMaxParts);
+  if (p.tiles * c->kv_heads >= (prompt ? wgs : kRowTiles) || p.tiles * max_pages > 0x3FFFFFFF) return p;
+  p.target = std::clamp(wgs / c->kv_heads, 1, kKvMaxParts);
   // parts that the counters and the workspace hold, for each head
   const size_t slot = (size_t)kv_part_floats(p.rows, c->head_dim) * 4;
-  const size_t room = workspace_bytes > BQ_KV_ATTN_COUNTER_BYTES ? (workspace_bytes - BQ_KV_ATTN_COUNTER_BYTES) / slot : 0;
-  p.target = std::min<int64_t>(p.target, (int64_t)(std::min(room, (size_t)kCounters) / c->kv_heads) - p.tiles);
+  size_t room = workspace_bytes > BQ_KV_ATTN_COUNTER_BYTES ? (workspace_bytes - BQ_KV_ATTN_COUNTER_BYTES) / slot : 0;
+  if (!prompt) room = std::min(room, (size_t)kCounters);
+  p.target = std::min<int64_t>(p.target, (int64_t)(room / c->kv_heads) - p.tiles);
   if (p.target < 2) p.target = 0;
   if (p.target > 0) p.bytes = BQ_KV_ATTN_COUNTER_BYTES + (size_t)((p.tiles + p.target) * c->kv_heads) * slot;
   return p;
@@ -113,15 +136,15 @@ int bq_kv_attn(const bq_kv_cache* cache, int layer, const void* q, void* out, lo
   p.counters = static_cast<unsigned*>(workspace);
   p.part = workspace ? reinterpret_cast<float*>(static_cast<char*>(workspace) + BQ_KV_ATTN_COUNTER_BYTES) : nullptr;
   const int64_t wgs = pl.tiles + pl.target;
-  if (wgs > 0x7FFFFFFF) return BQ_ERR_SHAPE;
-  return kv_launch(pick_rows(D, pl.rows, cache->format), 
-#ifdef XG
-dim3((unsigned)wgs, (unsigned)cache->kv_heads)
-#else
-dim3((unsigned)cache->kv_heads, (unsigned)wgs)
-#endif
-,
-                   dim3((unsigned)(64 * kv_waves(D))), 0, stream, &p);
+  if (wgs * (kPromptRows / 16) > 0x7FFFFFFF) return BQ_ERR_SHAPE;
+  if (pl.rows != kPromptRows)
+    return kv_launch(pick_rows(D, pl.rows, cache->format), dim3((unsigned)cache->kv_heads, (unsigned)wgs),
+                     dim3((unsigned)(64 * kv_waves(D))), 0, stream, &p);
+  st = kv_launch(pick_prompt(D, cache->format), dim3((unsigned)cache->kv_heads, (unsigned)wgs), dim3(kPromptThreads), 0,
+                 stream, &p);
+  if (st != BQ_OK || pl.target == 0) return st;
+  return kv_launch(pick_join(D), dim3((unsigned)cache->kv_heads, (unsigned)(wgs * (kPromptRows / 16))), dim3(256), 0,
+                   stream, &p);
 }
 
 }  // extern "C"

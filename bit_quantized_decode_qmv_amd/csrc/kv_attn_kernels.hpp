@@ -94,7 +94,7 @@ __device__ __forceinline__ bool kv_attn_work(const KvAttnParams& p, int item, Kv
     // heads of 128: 16 pages 10.0 us in one part and 11.9 in two; 32 pages
     // 14.4 us in parts of 16 and 11.9 in parts of 8; 2047 pages of one head
     // 28.6 us in parts of 16 and 41.1 in parts of 8)
-    const int least = all <= 16 || all > 64 ? 16 : 8;
+    const int least = ROWS > 32 ? 4 : all <= 16 || all > 64 ? 16 : 8;
     w.chunk = max((int)(((unsigned)all + p.target - 1) / (unsigned)p.target), least);
   }
   // whole parts ahead of a tile's last one
@@ -108,6 +108,7 @@ __device__ __forceinline__ bool kv_attn_work(const KvAttnParams& p, int item, Kv
     w.s.len = __builtin_amdgcn_readlane(s.len, at);
     w.parts = (p.target > 0 ? __builtin_amdgcn_readlane(whole(s), at) : 0) + 1;
     w.slot = before + w.tile * w.parts;
+    w.tile = __builtin_amdgcn_readlane(tiles(s), at) - 1 - w.tile;  // the last rows see the most: they begin first
   };
   int wholes = 0;
   if (p.target > 0) {
@@ -172,6 +173,19 @@ __device__ __forceinline__ kv_rsrc_t kv_rsrc(const void* base, int bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, bytes, 0x00020000);
 }
 
+// Table entries of pages at first, first + step, ..: a lane holds one of 64.
+struct KvPages {
+  int ids;
+  // page id of entry k (asked for in order); -1 past `end` or where the table holds no page
+  __device__ __forceinline__ int at(const KvAttnParams& p, int b, int first, int step, int end, int k) {
+    if ((k & 63) == 0) {
+      const int place = first + step * (k + ((int)threadIdx.x & 63));
+      ids = place < end ? kv_page(p.batch, b, place) : -1;
+    }
+    return __builtin_amdgcn_readlane(ids, k & 63);
+  }
+};
+
 // One page's codes in flight or at hand, as a wave holds them.
 template <int D>
 struct KvCodes {
@@ -219,9 +233,11 @@ __global__ __launch_bounds__(64 * kv_waves(D)) void kv_attn_rows_kernel(KvAttnPa
   const int begin = pa + (w.parts > 1 ? w.split * w.chunk : 0);
   const int end = pa + (w.split == w.parts - 1 ? pages : min((w.split + 1) * w.chunk, pages));
 
-  // requests of a page: its place in the cache, or none
-  const auto place = [&](int at) -> int64_t {
-    const int page = at < end ? kv_page(p.batch, w.b, at) : -1;
+  // The wave's k-th page is at begin + wave + NW k.  A lane holds the table's
+  // entry of one of 64 of them, so that no request waits for the table.
+  KvPages pages_of;
+  const auto place = [&](int k) -> int64_t {
+    const int page = pages_of.at(p, w.b, begin + wave, NW, end, k);
     return page < 0 ? -1 : (int64_t)page * p.kv_heads + head;
   };
   KvCodes<D> x;
@@ -236,8 +252,14 @@ __global__ __launch_bounds__(64 * kv_waves(D)) void kv_attn_rows_kernel(KvAttnPa
 #pragma unroll
     for (int n = 0; n < N; ++n) x.v[n] = __builtin_amdgcn_raw_buffer_load_b128(rs, lane * 16, n * 1024, 0);
   };
-  int64_t here = place(begin + wave);
+  f32x4 sk, sv;
+  const auto load_scales = [&](int64_t at) {
+    sk = *reinterpret_cast<const f32x4*>(p.ks + max(at, (int64_t)0) * kKvBlocks);
+    sv = *reinterpret_cast<const f32x4*>(p.vs + max(at, (int64_t)0) * kKvBlocks);
+  };
+  int64_t here = place(0);
   load_k(here);
+  load_scales(here);
   load_v(here);
 
   // Q as the B operand: column r, k = dims 64c + 16g + 8h .. + 7
@@ -268,11 +290,8 @@ __global__ __launch_bounds__(64 * kv_waves(D)) void kv_attn_rows_kernel(KvAttnPa
     for (int n = 0; n < N; ++n) o[t][n] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
 
-  for (int at = begin + wave; at < end; at += NW) {
-    const int64_t next = place(at + NW);
-    const int64_t ph = max(here, (int64_t)0);
-    const f32x4 skv = *reinterpret_cast<const f32x4*>(p.ks + ph * kKvBlocks);
-    f32x4 sv = *reinterpret_cast<const f32x4*>(p.vs + ph * kKvBlocks);
+  for (int at = begin + wave, k = 1; at < end; at += NW, ++k) {
+    const int64_t next = place(k);
     const int j0 = at * kKvPage;
     const int left = here < 0 ? 0 : s.len - j0;  // tokens of the page that are held
 
@@ -292,11 +311,11 @@ __global__ __launch_bounds__(64 * kv_waves(D)) void kv_attn_rows_kernel(KvAttnPa
         }
       }
     }
-    load_k(next);
 #pragma unroll
     for (int t = 0; t < RT; ++t)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y[t][i] *= skv[i] * p.scale;
+      for (int i = 0; i < 4; ++i) y[t][i] *= sk[i] * p.scale;
+    load_k(next);
     if (left < kKvPage || j0 + kKvPage > r0.hi || j0 < r1.lo) {
       // a page that some row does not see whole: the row's tokens [lo, hi)
       // as one unsigned comparison of each token
@@ -363,6 +382,7 @@ __global__ __launch_bounds__(64 * kv_waves(D)) void kv_attn_rows_kernel(KvAttnPa
     }
     half8_t ph_[RT][2], pl_[RT][2];
     const f32x4 unit = sv * invR;
+    load_scales(next);
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
       const float base = m[t] == -__builtin_inff() ? 0.f : m[t];  // a row that has seen nothing yet

@@ -1,0 +1,326 @@
+// Attention of many rows over the paged 8-bit cache: a prompt's chunk, a
+// whole prompt, or queries over an encoder's states.
+//
+// The same products as for few rows (S^T = K Q^T, O^T += V^T P^T, 32 rows a
+// wave), bound by the matrix cores and, about equally, by the vector units'
+// softmax.  What differs is the sharing: a workgroup's four waves take 128
+// rows and walk the pages together, so that a page's codes are read and
+// turned into fp16 once for all of them.  The fp16 operands go through LDS in
+// the order in which the waves read them back (16 bytes a lane, consecutive:
+// no bank is hit twice); the next page's codes are in flight meanwhile, and
+// two workgroups share a CU where their registers and LDS allow, one in its
+// products while the other is in its softmax.
+//
+// The probabilities are rounded to fp16 (nearest even) once, with V's block
+// scale folded in: 2^-12 of each on average, as the rounding of the result.
+#pragma once
+
+#include "kv_attn_kernels.hpp"
+
+namespace bq {
+
+#ifndef XA
+#define XA 8
+#endif
+// The order of a product whose operands come from LDS: AHEAD reads first,
+// then one more after each pair of matrix instructions, so that no pair waits
+// for the read just issued.
+template <int READS>
+__device__ __forceinline__ void kv_order_reads() {
+  constexpr int AHEAD = READS < 2 * XA ? READS / 2 : XA;
+  __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);  // LDS reads
+#pragma unroll
+  for (int i = 0; i < READS - AHEAD; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);  // matrix instructions
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(0x008, 2 * AHEAD, 0);
+}
+
+constexpr int kPromptWaves = 4, kPromptThreads = 64 * kPromptWaves;
+constexpr int kPromptRows = 32 * kPromptWaves;
+
+template <int D, int FMT>
+__global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prompt_kernel(KvAttnParams p) {
+  constexpr int C = D / 64, N = D / 16, UNITS = 4 * D / kPromptThreads;  // 16-byte units of K (or V) a thread
+  // [buffer][K, V][operand][lane][8]
+  __shared__ __align__(16) half8_t lds[2][2][8 * C][64];
+  const int lane = (int)threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int head = (int)blockIdx.x;
+  const int item = (int)blockIdx.y;
+  KvWork w;
+  if (!kv_attn_work<kPromptRows>(p, item, w)) return;
+  const KvSeq s = w.s;
+  const int rows = s.n * p.group;
+  const int row0 = w.tile * kPromptRows, row1 = min(row0 + kPromptRows, rows) - 1;
+  const KvRowRange r0 = kv_row_range(p, s, row0 / p.group), r1 = kv_row_range(p, s, row1 / p.group);
+  const int pa = r0.lo / kKvPage, pages = max((r1.hi + kKvPage - 1) / kKvPage - pa, 0);
+  const int begin = pa + (w.parts > 1 ? w.split * w.chunk : 0);
+  const int end = pa + (w.split == w.parts - 1 ? pages : min((w.split + 1) * w.chunk, pages));
+
+  KvPages pages_of;
+  const auto place = [&](int k) -> int64_t {
+    const int page = pages_of.at(p, w.b, begin, 1, end, k);
+    return page < 0 ? -1 : (int64_t)page * p.kv_heads + head;
+  };
+  // a page's scales are requested ahead of its codes: what waits for them
+  // does not wait for the codes
+  f32x4 sk_next, sv_next;
+  u32x4_t raw[2][UNITS];
+  const auto request = [&](int64_t at) {
+    sk_next = *reinterpret_cast<const f32x4*>(p.ks + max(at, (int64_t)0) * kKvBlocks);
+    sv_next = *reinterpret_cast<const f32x4*>(p.vs + max(at, (int64_t)0) * kKvBlocks);
+    const kv_rsrc_t rk = kv_rsrc(p.k + max(at, (int64_t)0) * (kKvPage * D), at < 0 ? 0 : kKvPage * D);
+    const kv_rsrc_t rv = kv_rsrc(p.v + max(at, (int64_t)0) * (kKvPage * D), at < 0 ? 0 : kKvPage * D);
+#pragma unroll
+    for (int j = 0; j < UNITS; ++j) {
+      raw[0][j] = __builtin_amdgcn_raw_buffer_load_b128(rk, (int)threadIdx.x * 16, j * kPromptThreads * 16, 0);
+      raw[1][j] = __builtin_amdgcn_raw_buffer_load_b128(rv, (int)threadIdx.x * 16, j * kPromptThreads * 16, 0);
+    }
+  };
+  // codes at hand to buffer `to`; `left` tokens of the page are held
+  const auto stage = [&](int to, int left) {
+#pragma unroll
+    for (int j = 0; j < UNITS; ++j) {
+      const int unit = (int)threadIdx.x + j * kPromptThreads, op = unit >> 6, ln = unit & 63;
+      if (FMT == BQ_KV_E4M3 && left < kKvPage) {
+        // what lies past the length may be no number: cleared
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int keep = min(max(left - 16 * i - 4 * (ln >> 4), 0), 4);
+          raw[1][j][i] &= keep == 4 ? 0xFFFFFFFFu : (1u << (8 * keep)) - 1u;
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        lds[to][x][2 * op][ln] = kv_half8<FMT>(raw[x][j][0], raw[x][j][1]);
+        lds[to][x][2 * op + 1][ln] = kv_half8<FMT>(raw[x][j][2], raw[x][j][3]);
+      }
+    }
+  };
+  int64_t here = place(0);
+  request(here);
+
+  // this wave's rows
+  half8_t q[2][2 * C];
+  int lo[2], hi[2];
+  int wave_lo = 0, wave_hi = 0;  // tokens that some row of the wave sees
+  int all_lo = 0, all_hi = 0;    // that all of them see
+  {
+    const int first = row0 + 32 * wave, last = min(first + 31, rows - 1);
+    if (first < rows) {
+      const KvRowRange a = kv_row_range(p, s, first / p.group), b = kv_row_range(p, s, last / p.group);
+      wave_lo = a.lo;
+      wave_hi = b.hi;
+      all_lo = b.lo;
+      all_hi = a.hi;
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int row = row0 + 32 * wave + 16 * t + r;
+    const bool ok = row < rows;
+    const int token = ok ? row / p.group : 0, qh = head * p.group + (ok ? row - token * p.group : 0);
+    const KvRowRange range = kv_row_range(p, s, token);
+    lo[t] = range.lo;
+    hi[t] = ok ? range.hi : 0;
+    const _Float16* src = p.q + (int64_t)(s.q0 + token) * p.q_stride + qh * D + 16 * g;
+#pragma unroll
+    for (int c = 0; c < 2 * C; ++c) {
+      q[t][c] = ok ? *reinterpret_cast<const half8_t*>(src + (c >> 1) * 64 + (c & 1) * 8) : half8_t{};
+      if (p.scale < 0.f) q[t][c] = -q[t][c];
+    }
+  }
+  const float scale = __builtin_fabsf(p.scale);
+
+  f32x4 o[2][N];
+  float m[2], l[2];
+  float R = 0x1p-100f, invR = 0x1p100f;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    m[t] = -__builtin_inff();
+    l[t] = 0.f;
+#pragma unroll
+    for (int n = 0; n < N; ++n) o[t][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+
+  stage(0, here < 0 ? 0 : s.len - begin * kKvPage);
+  __syncthreads();
+  for (int at = begin; at < end; ++at) {
+    const int buf = (at - begin) & 1;
+    const int64_t next = place(at + 1 - begin);
+    const f32x4 sk = sk_next;
+    f32x4 sv = sv_next;
+    request(next);
+    const int j0 = at * kKvPage, left = here < 0 ? 0 : s.len - j0;
+
+    if (j0 < wave_hi && j0 + kKvPage > wave_lo) {
+      f32x4 y[2][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        y[0][i] = y[1][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 2 * C; ++c) {
+          const half8_t a = lds[buf][0][2 * C * i + c][lane];
+          y[0][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, q[0][c], y[0][i], 0, 0, 0);
+          y[1][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, q[1][c], y[1][i], 0, 0, 0);
+        }
+      }
+      kv_order_reads<8 * C>();
+      f32x4 c = sk * scale;
+      if (left < kKvPage || j0 + kKvPage > all_hi || j0 < all_lo) {
+        // a page that some row does not see whole; a block past the length
+        // has no scale
+        if (left < kKvPage) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (16 * i >= left) sv[i] = c[i] = 0.f;
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int from = max(lo[t] - j0, 0), count = max(min(hi[t] - j0, left) - from, 0);
+          int in = 4 * g - from;
+          asm volatile("" : "+v"(in));
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              y[t][i][e] = (unsigned)(in + 16 * i + e) < (unsigned)count ? y[t][i][e] * c[i] : -__builtin_inff();
+        }
+        c = f32x4{1.f, 1.f, 1.f, 1.f};  // a hidden score times 0 would be no number
+      }
+      const float rmax = __builtin_fmaxf(__builtin_fmaxf(sv[0], sv[1]), __builtin_fmaxf(sv[2], sv[3]));
+      float mx[2];
+      bool raise = rmax > R;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        mx[t] = -__builtin_inff();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float top = __builtin_fmaxf(__builtin_fmaxf(y[t][i][0], y[t][i][1]), __builtin_fmaxf(y[t][i][2], y[t][i][3]));
+          mx[t] = __builtin_fmaxf(mx[t], top * c[i]);
+        }
+        raise = raise || mx[t] > m[t] + 8.f;
+      }
+      if (__ballot(raise) != 0) {
+        float change = 1.f;
+        if (rmax > R) {
+          const int ex = (int)((__builtin_bit_cast(uint32_t, rmax) >> 23) & 255u) + 1;
+          const float up = __builtin_bit_cast(float, (uint32_t)min(ex, 253) << 23);
+          change = R / up;
+          R = up;
+          invR = 1.f / up;
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const float mn = __builtin_fmaxf(m[t], kv_col_max(mx[t]));
+          const float alpha = mn == -__builtin_inff() ? 1.f : kv_exp2(m[t] - mn);
+          m[t] = mn;
+          l[t] *= alpha;
+#pragma unroll
+          for (int n = 0; n < N; ++n) o[t][n] *= alpha * change;
+        }
+      }
+      half8_t pb[2][2];
+      const f32x4 unit = sv * invR;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const float base = m[t] == -__builtin_inff() ? 0.f : m[t];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float e2 = kv_exp2(__builtin_fmaf(y[t][i][e], c[i], -base));
+            l[t] += e2;
+            pb[t][i >> 1][(i & 1) * 4 + e] = (_Float16)(e2 * unit[i]);
+          }
+      }
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const half8_t a = lds[buf][1][2 * n + h][lane];
+          o[0][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pb[0][h], o[0][n], 0, 0, 0);
+          o[1][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pb[1][h], o[1][n], 0, 0, 0);
+        }
+      kv_order_reads<2 * N>();
+    }
+    stage(buf ^ 1, next < 0 ? 0 : s.len - j0 - kKvPage);
+    here = next;
+    __syncthreads();
+  }
+
+  constexpr int SLOT = kv_part_floats(kPromptRows, D);
+  float* mine = p.part + ((int64_t)(w.slot + w.split) * p.kv_heads + head) * SLOT;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const float sum = kv_col_sum(l[t]);
+    const int in = 32 * wave + 16 * t + r, row = row0 + in;
+    if (row >= rows) continue;
+    if (w.parts == 1) {
+      const int token = row / p.group, qh = head * p.group + row - token * p.group;
+      const float inv = sum > 0.f ? R / sum : 0.f;  // nothing seen: zeros
+      _Float16* dst = p.out + (int64_t)(s.q0 + token) * p.out_stride + qh * D + 4 * g;
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const f32x4 v = o[t][n] * inv;
+        *reinterpret_cast<half4_t*>(dst + 16 * n) = half4_t{(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
+      }
+    } else {
+      if (g == 0) *reinterpret_cast<float2*>(mine + 2 * in) = make_float2(m[t], sum);
+#pragma unroll
+      for (int n = 0; n < N; ++n) *reinterpret_cast<f32x4*>(mine + 2 * kPromptRows + in * D + 16 * n + 4 * g) = o[t][n] * R;
+    }
+  }
+}
+
+// Joins the parts of the tiles that have several, in order; a workgroup takes
+// 16 rows of a tile, found as the product's workgroups find theirs (the
+// workgroup of a tile's last part).
+template <int D>
+__global__ __launch_bounds__(256) void kv_attn_join_kernel(KvAttnParams p) {
+  constexpr int SLOT = kv_part_floats(kPromptRows, D);
+  __shared__ float f[kKvMaxParts][16];
+  const int head = (int)blockIdx.x, item = (int)blockIdx.y / (kPromptRows / 16), first = (int)blockIdx.y % (kPromptRows / 16) * 16;
+  KvWork w;
+  if (!kv_attn_work<kPromptRows>(p, item, w) || w.split != w.parts - 1 || w.parts == 1) return;
+  const KvSeq s = w.s;
+  const int row0 = w.tile * kPromptRows + first, some = min(16, s.n * p.group - row0);
+  if (some <= 0) return;
+  const int64_t next = (int64_t)p.kv_heads * SLOT;
+  const float* part0 = p.part + ((int64_t)w.slot * p.kv_heads + head) * SLOT;
+  // 16 lanes a row
+  const int row = (int)threadIdx.x >> 4, sub = (int)threadIdx.x & 15;
+  float mx = -__builtin_inff(), sum = 0.f;
+  if (row < some) {
+    for (int i = sub; i < w.parts; i += 16) mx = __builtin_fmaxf(mx, part0[i * next + 2 * (first + row)]);
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) mx = __builtin_fmaxf(mx, __shfl_xor(mx, d, 64));
+    const float base = mx == -__builtin_inff() ? 0.f : mx;
+    for (int i = sub; i < w.parts; i += 16) {
+      const float2 ml = *reinterpret_cast<const float2*>(part0 + i * next + 2 * (first + row));
+      const float e = kv_exp2(ml.x - base);
+      f[i][row] = e;
+      sum += ml.y * e;
+    }
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor(sum, d, 64);
+  }
+  __syncthreads();
+  if (row >= some) return;
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const int token = (row0 + row) / p.group, qh = head * p.group + row0 + row - token * p.group;
+  _Float16* dst = p.out + (int64_t)(s.q0 + token) * p.out_stride + qh * D;
+#pragma unroll
+  for (int d = 4 * sub; d < D; d += 64) {
+    f32x4 y = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int i = 0; i < w.parts; ++i)
+      y += *reinterpret_cast<const f32x4*>(part0 + i * next + 2 * kPromptRows + (first + row) * D + d) * f[i][row];
+    y *= inv;
+    *reinterpret_cast<half4_t*>(dst + d) = half4_t{(_Float16)y[0], (_Float16)y[1], (_Float16)y[2], (_Float16)y[3]};
+  }
+}
+
+}  // namespace bq
