@@ -29,6 +29,7 @@ struct KvAttnParams {
   unsigned* counters;    // workspace: parts done of each tile, zero between calls
   float* part;           // workspace: partial results
   int target;            // workgroups of a head to aim at; 0: tiles are not split
+  int min_pages;         // of a part; 0: by the number of pages
 };
 
 constexpr int kKvMaxParts = 128;  // of a tile
@@ -43,6 +44,21 @@ __device__ __forceinline__ float kv_col_max(float x) {
 __device__ __forceinline__ float kv_col_sum(float x) {
   x += __shfl_xor(x, 16, 64);
   return x + __shfl_xor(x, 32, 64);
+}
+
+__device__ __forceinline__ float kv_max3(float a, float b, float c) {
+  float d;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "v"(c));  // (without quieting each operand first)
+  return d;
+}
+// R becomes the power of two above the scale rmax, invR its reciprocal; what
+// values in units of the old one are multiplied by.
+__device__ __forceinline__ float kv_raise_unit(float rmax, float& R, float& invR) {
+  const uint32_t ex = min(((__builtin_bit_cast(uint32_t, rmax) >> 23) & 255u) + 1, 253u);
+  const float was = R;
+  R = __builtin_bit_cast(float, ex << 23);
+  invR = __builtin_bit_cast(float, (254u - ex) << 23);
+  return was * invR;
 }
 
 // Values that other workgroups read: stores and loads at device scope, which
@@ -72,7 +88,8 @@ __device__ __forceinline__ int kv_first_page(const KvAttnParams& p, const KvSeq&
 }
 // Every wave of the grid finds its share from the batch's arrays: a lane
 // takes a sequence (64 at a time; the first 64 stay in its registers).
-template <int ROWS>
+// JOIN: share `item` is the last part of tile `item`.
+template <int ROWS, bool JOIN = false>
 __device__ __forceinline__ bool kv_attn_work(const KvAttnParams& p, int item, KvWork& w) {
   const int lane = (int)threadIdx.x & 63, batch = p.batch.batch;
   const auto pages = [&](const KvSeq& s) {
@@ -90,11 +107,11 @@ __device__ __forceinline__ bool kv_attn_work(const KvAttnParams& p, int item, Kv
     int all = 0;
     for (int base = 0; base < batch; base += 64) all += tiles(seq(base)) * pages(seq(base));
     all = __builtin_amdgcn_readlane(kv_scan(all), 63);
-    // no part shorter than pays for joining it (measured, one sequence, 8
-    // heads of 128: 16 pages 10.0 us in one part and 11.9 in two; 32 pages
-    // 14.4 us in parts of 16 and 11.9 in parts of 8; 2047 pages of one head
-    // 28.6 us in parts of 16 and 41.1 in parts of 8)
-    const int least = ROWS > 32 ? 4 : all <= 16 || all > 64 ? 16 : 8;
+    // few rows: no part shorter than pays for joining it (measured, one
+    // sequence, 8 heads of 128: 16 pages 10.0 us in one part and 11.9 in two;
+    // 32 pages 14.4 us in parts of 16 and 11.9 in parts of 8; 2047 pages of
+    // one head 28.6 us in parts of 16 and 41.1 in parts of 8)
+    const int least = p.min_pages > 0 ? p.min_pages : all <= 16 || all > 64 ? 16 : 8;
     w.chunk = max((int)(((unsigned)all + p.target - 1) / (unsigned)p.target), least);
   }
   // whole parts ahead of a tile's last one
@@ -118,7 +135,7 @@ __device__ __forceinline__ bool kv_attn_work(const KvAttnParams& p, int item, Kv
       const int nt = tiles(s), nw = nt * whole(s);
       const int st = kv_scan(nt), sw = kv_scan(nw);
       const int all_w = __builtin_amdgcn_readlane(sw, 63);
-      if (item < wholes + all_w) {
+      if (!JOIN && item < wholes + all_w) {
         const int at = __builtin_ctzll(__ballot(wholes + sw > item));
         const int from = wholes + __builtin_amdgcn_readlane(sw - nw, at);
         const int each = __builtin_amdgcn_readlane(whole(s), at);
@@ -131,6 +148,7 @@ __device__ __forceinline__ bool kv_attn_work(const KvAttnParams& p, int item, Kv
       before_tiles += __builtin_amdgcn_readlane(st, 63);
     }
   }
+  if (JOIN) item += wholes;
   int before_tiles = 0, before_wholes = 0;
   for (int base = 0; base < batch; base += 64) {
     const KvSeq s = seq(base);
@@ -355,21 +373,11 @@ __global__ __launch_bounds__(64 * kv_waves(D)) void kv_attn_rows_kernel(KvAttnPa
     for (int t = 0; t < RT; ++t) {
       mx[t] = y[t][0][0];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) mx[t] = __builtin_fmaxf(mx[t], y[t][i][e]);
+      for (int i = 0; i < 4; ++i) mx[t] = kv_max3(kv_max3(mx[t], y[t][i][0], y[t][i][1]), y[t][i][2], y[t][i][3]);
       raise = raise || mx[t] > m[t] + 8.f;
     }
     if (__ballot(raise) != 0) {
-      float change = 1.f;
-      if (rmax > R) {
-        // the power of two above the largest scale
-        const int ex = (int)((__builtin_bit_cast(uint32_t, rmax) >> 23) & 255u) + 1;
-        const float up = __builtin_bit_cast(float, (uint32_t)min(ex, 253) << 23);
-        change = R / up;
-        R = up;
-        invR = 1.f / up;
-      }
+      const float change = rmax > R ? kv_raise_unit(rmax, R, invR) : 1.f;
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
         const float mn = __builtin_fmaxf(m[t], kv_col_max(mx[t]));

@@ -13,21 +13,20 @@
 //
 // The probabilities are rounded to fp16 (nearest even) once, with V's block
 // scale folded in: 2^-12 of each on average, as the rounding of the result.
+// Their sum is taken of the rounded ones, so that a row that sees few tokens
+// does not keep the rounding of a common factor.
 #pragma once
 
 #include "kv_attn_kernels.hpp"
 
 namespace bq {
 
-#ifndef XA
-#define XA 8
-#endif
 // The order of a product whose operands come from LDS: AHEAD reads first,
-// then one more after each pair of matrix instructions, so that no pair waits
-// for the read just issued.
+// then one more after the two matrix instructions that share one, so that
+// none waits for the read just issued.
 template <int READS>
 __device__ __forceinline__ void kv_order_reads() {
-  constexpr int AHEAD = READS < 2 * XA ? READS / 2 : XA;
+  constexpr int AHEAD = READS < 16 ? READS / 2 : 8;
   __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);  // LDS reads
 #pragma unroll
   for (int i = 0; i < READS - AHEAD; ++i) {
@@ -171,11 +170,14 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
       f32x4 c = sk * scale;
       if (left < kKvPage || j0 + kKvPage > all_hi || j0 < all_lo) {
         // a page that some row does not see whole; a block past the length
-        // has no scale
+        // has no scale (its probabilities are 0 under any)
         if (left < kKvPage) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (16 * i >= left) sv[i] = c[i] = 0.f;
+            if (16 * i >= left) {
+              c[i] = 0.f;
+              sv[i] = left > 0 ? sv[0] : 0.f;
+            }
         }
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -198,20 +200,13 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
         mx[t] = -__builtin_inff();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float top = __builtin_fmaxf(__builtin_fmaxf(y[t][i][0], y[t][i][1]), __builtin_fmaxf(y[t][i][2], y[t][i][3]));
+          const float top = kv_max3(kv_max3(y[t][i][0], y[t][i][1], y[t][i][2]), y[t][i][3], y[t][i][3]);
           mx[t] = __builtin_fmaxf(mx[t], top * c[i]);
         }
         raise = raise || mx[t] > m[t] + 8.f;
       }
       if (__ballot(raise) != 0) {
-        float change = 1.f;
-        if (rmax > R) {
-          const int ex = (int)((__builtin_bit_cast(uint32_t, rmax) >> 23) & 255u) + 1;
-          const float up = __builtin_bit_cast(float, (uint32_t)min(ex, 253) << 23);
-          change = R / up;
-          R = up;
-          invR = 1.f / up;
-        }
+        const float change = rmax > R ? kv_raise_unit(rmax, R, invR) : 1.f;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           const float mn = __builtin_fmaxf(m[t], kv_col_max(mx[t]));
@@ -223,18 +218,48 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
         }
       }
       half8_t pb[2][2];
-      const f32x4 unit = sv * invR;
+      // V's scale in units of R goes into the exponent, and a block's sum is
+      // divided by it once.  Scales below 2^-40 R count as that: their
+      // probabilities are 0 in fp16 either way.
+      f32x4 log_unit, per_unit;
+      bool fine = true;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float unit = __builtin_fmaxf(sv[i] * invR, 0x1p-40f);
+        fine = fine && unit >= 0x1p-6f;
+        log_unit[i] = __builtin_amdgcn_logf(unit);
+        per_unit[i] = __builtin_amdgcn_rcpf(unit);
+      }
+      float base[2];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const float base = m[t] == -__builtin_inff() ? 0.f : m[t];
+        base[t] = m[t] == -__builtin_inff() ? 0.f : m[t];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float e2 = kv_exp2(__builtin_fmaf(y[t][i][e], c[i], -base));
-            l[t] += e2;
-            pb[t][i >> 1][(i & 1) * 4 + e] = (_Float16)(e2 * unit[i]);
+          for (int e = 0; e < 4; ++e)
+            pb[t][i >> 1][(i & 1) * 4 + e] = (_Float16)kv_exp2(__builtin_fmaf(y[t][i][e], c[i], log_unit[i] - base[t]));
+      }
+      if (__builtin_amdgcn_readfirstlane(fine)) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const half8_t v = pb[t][i >> 1];
+            const half2_t one = {(_Float16)1.f, (_Float16)1.f};
+            const half2_t a = i & 1 ? half2_t{v[4], v[5]} : half2_t{v[0], v[1]}, b = i & 1 ? half2_t{v[6], v[7]} : half2_t{v[2], v[3]};
+            const float sum = __builtin_amdgcn_fdot2(a, one, __builtin_amdgcn_fdot2(b, one, 0.f, false), false);
+            l[t] = __builtin_fmaf(sum, per_unit[i], l[t]);
           }
+      } else {
+        // a block of V far below the others: its rounded probabilities say
+        // too little of their sum
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) l[t] += kv_exp2(__builtin_fmaf(y[t][i][e], c[i], -base[t]));
       }
 #pragma unroll
       for (int n = 0; n < N; ++n)
@@ -276,15 +301,14 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
 }
 
 // Joins the parts of the tiles that have several, in order; a workgroup takes
-// 16 rows of a tile, found as the product's workgroups find theirs (the
-// workgroup of a tile's last part).
+// 16 rows of a tile.
 template <int D>
 __global__ __launch_bounds__(256) void kv_attn_join_kernel(KvAttnParams p) {
   constexpr int SLOT = kv_part_floats(kPromptRows, D);
   __shared__ float f[kKvMaxParts][16];
   const int head = (int)blockIdx.x, item = (int)blockIdx.y / (kPromptRows / 16), first = (int)blockIdx.y % (kPromptRows / 16) * 16;
   KvWork w;
-  if (!kv_attn_work<kPromptRows>(p, item, w) || w.split != w.parts - 1 || w.parts == 1) return;
+  if (!kv_attn_work<kPromptRows, true>(p, item, w) || w.parts == 1) return;
   const KvSeq s = w.s;
   const int row0 = w.tile * kPromptRows + first, some = min(16, s.n * p.group - row0);
   if (some <= 0) return;
