@@ -154,20 +154,25 @@ __device__ __forceinline__ int kv_scan(int v) {
   return v;
 }
 
-// Item `item` of a list in which sequence b has count(b) items: the sequence
-// and the item's place among its own.  Called by whole waves; every lane gets
-// the same (scalar) answer; false past the list's end.
+// Item `item` of a list in which a sequence has count(sequence) items: the
+// sequence, its number and the item's place among its own.  Called by whole
+// waves, a lane a sequence; every lane gets the same (scalar) answer; false
+// past the list's end.
 template <typename Count>
-__device__ __forceinline__ bool kv_locate(int item, int batch, Count count, int& b, int& local) {
+__device__ __forceinline__ bool kv_locate(const KvBatch& p, int item, Count count, KvSeq& s, int& b, int& local) {
   const int lane = threadIdx.x & 63;
-  for (int base = 0; base < batch; base += 64) {
-    const int c = base + lane < batch ? count(base + lane) : 0;
-    const int s = kv_scan(c);
-    const int all = __builtin_amdgcn_readlane(s, 63);
+  for (int base = 0; base < p.batch; base += 64) {
+    const KvSeq mine = base + lane < p.batch ? kv_seq(p, base + lane) : KvSeq{};
+    const int c = base + lane < p.batch ? count(mine) : 0;
+    const int sum = kv_scan(c);
+    const int all = __builtin_amdgcn_readlane(sum, 63);
     if (item < all) {
-      const int at = __builtin_ctzll(__ballot(s > item));
+      const int at = __builtin_ctzll(__ballot(sum > item));
       b = base + at;
-      local = item - (__builtin_amdgcn_readlane(s, at) - __builtin_amdgcn_readlane(c, at));
+      local = item - __builtin_amdgcn_readlane(sum - c, at);
+      s.q0 = __builtin_amdgcn_readlane(mine.q0, at);
+      s.n = __builtin_amdgcn_readlane(mine.n, at);
+      s.len = __builtin_amdgcn_readlane(mine.len, at);
       return true;
     }
     item -= all;
