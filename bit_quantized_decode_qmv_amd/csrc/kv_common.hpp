@@ -186,7 +186,7 @@ inline bool kv_aligned(const void* p, uintptr_t a) { return (reinterpret_cast<ui
 inline int kv_check_cache(const bq_kv_cache* c) {
   if (!c || !c->k || !c->v || !c->k_scales || !c->v_scales) return BQ_ERR_NULL;
   if (c->format != BQ_KV_I8 && c->format != BQ_KV_E4M3) return BQ_ERR_BITS;
-  if (c->layers < 1 || c->num_pages < 1 || c->num_pages > BQ_KV_MAX_PAGES || c->kv_heads < 1 || c->kv_heads > 1024 ||
+  if (c->layers < 1 || c->layers > 4096 || c->num_pages < 1 || c->num_pages > BQ_KV_MAX_PAGES || c->kv_heads < 1 || c->kv_heads > 1024 ||
       (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 192 && c->head_dim != 256))
     return BQ_ERR_SHAPE;
   if (!kv_aligned(c->k, 16) || !kv_aligned(c->v, 16) || !kv_aligned(c->k_scales, 16) || !kv_aligned(c->v_scales, 16))

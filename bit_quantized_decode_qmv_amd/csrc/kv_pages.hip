@@ -20,11 +20,13 @@ KvPool pool_of(const bq_kv_cache* c) {
   return p;
 }
 
-// workgroups of the second launch: as many as hold one unit each of the most
-// that can be copied, at most eight for each CU
-unsigned copy_grid(const KvPool& p, int64_t most) {
+// Workgroups of the launch that copies, for `most` pairs at most: a unit of
+// one pair each, up to sixteen for each CU, from where on they take several
+// pairs.
+dim3 copy_grid(const KvPool& p, int64_t most) {
   const int64_t units = (p.page_bytes + kCopyUnit - 1) / kCopyUnit;
-  return (unsigned)std::clamp<int64_t>(most * p.layers * 2 * units, 64, 2048);
+  const int64_t pairs = std::clamp<int64_t>(4096 / (units * p.layers * 2), 1, std::max<int64_t>(most, 1));
+  return dim3((unsigned)(units * pairs), (unsigned)(p.layers * 2));
 }
 
 int check_tables(const bq_kv_cache* cache, const int* table, const int* refs, int rows, int max_pages, const int* status,
@@ -58,9 +60,9 @@ KvPagesParams params_of(const bq_kv_cache* c, int* table, int* lens, int* refs, 
   return p;
 }
 
-int run(const void* plan, const void* carry, unsigned grid, KvPagesParams& p, void* stream) {
+int run(const void* plan, const void* carry, dim3 grid, KvPagesParams& p, void* stream) {
   const int st = kv_launch(plan, dim3(1), dim3(kPlanThreads), 0, stream, &p);
-  return st != BQ_OK ? st : kv_launch(carry, dim3(grid), dim3(kCopyThreads), 0, stream, &p);
+  return st != BQ_OK ? st : kv_launch(carry, grid, dim3(kCopyThreads), 0, stream, &p);
 }
 
 }  // namespace
@@ -125,7 +127,7 @@ int bq_kv_copy_pages(const bq_kv_cache* cache, const int* src, const int* dst, i
   p.a = src;
   p.b = dst;
   p.n = n;
-  return kv_launch(reinterpret_cast<const void*>(&kv_copy_kernel), dim3(copy_grid(p.pool, n)), dim3(kCopyThreads), 0,
+  return kv_launch(reinterpret_cast<const void*>(&kv_copy_kernel), copy_grid(p.pool, n), dim3(kCopyThreads), 0,
                    stream, &p);
 }
 

@@ -237,30 +237,29 @@ __global__ __launch_bounds__(kPlanThreads) void kv_compact_plan_kernel(KvPagesPa
   plan_say(p, 1, up, 0);
 }
 
-// Copies of pages over all layers, a unit of kCopyUnit bytes a workgroup at a
-// time.  Ids out of range (the caller's own lists) are skipped.
+// Copies of pages over all layers.  The grid's y is a layer's K or V, its x a
+// unit of kCopyUnit bytes of every (gridDim.x / units)-th pair.  Ids out of
+// range (the caller's own lists) are skipped.
 __device__ __forceinline__ void copy_pages(const KvPool& c, const int* src, const int* dst, int count) {
-  const int units = (int)((c.page_bytes + kCopyUnit - 1) / kCopyUnit);
-  const int64_t all = (int64_t)count * c.layers * 2 * units;
-  for (int64_t i = blockIdx.x; i < all; i += gridDim.x) {
-    const int unit = (int)(i % units);
-    const int64_t j = i / units;
-    const int which = (int)(j & 1), layer = (int)((j >> 1) % c.layers), pair = (int)((j >> 1) / c.layers);
+  const unsigned units = (unsigned)((c.page_bytes + kCopyUnit - 1) / kCopyUnit);
+  const unsigned first = blockIdx.x / units, unit = blockIdx.x - first * units, step = gridDim.x / units;
+  const int which = (int)blockIdx.y & 1, layer = (int)blockIdx.y >> 1;
+  uint8_t* codes = which ? c.v : c.k;
+  float* scales = which ? c.vs : c.ks;
+  const int64_t at = (int64_t)unit * kCopyUnit + threadIdx.x * 16;
+  for (unsigned pair = first; pair < (unsigned)count; pair += step) {
     const int from = src[pair], to = dst[pair];
     if ((unsigned)from >= (unsigned)c.num_pages || (unsigned)to >= (unsigned)c.num_pages || from == to) continue;
     const int64_t fp = (int64_t)layer * c.num_pages + from, tp = (int64_t)layer * c.num_pages + to;
-    uint8_t* codes = which ? c.v : c.k;
-    float* scales = which ? c.vs : c.ks;
-    const int64_t at = (int64_t)unit * kCopyUnit + threadIdx.x * 16;
+    const uint8_t* f = codes + fp * c.page_bytes + at;
+    uint8_t* t = codes + tp * c.page_bytes + at;
     uint4 w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      if (at + e * kCopyThreads * 16 < c.page_bytes)
-        w[e] = *reinterpret_cast<const uint4*>(codes + fp * c.page_bytes + at + e * kCopyThreads * 16);
+      if (at + e * kCopyThreads * 16 < c.page_bytes) w[e] = *reinterpret_cast<const uint4*>(f + e * kCopyThreads * 16);
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      if (at + e * kCopyThreads * 16 < c.page_bytes)
-        *reinterpret_cast<uint4*>(codes + tp * c.page_bytes + at + e * kCopyThreads * 16) = w[e];
+      if (at + e * kCopyThreads * 16 < c.page_bytes) *reinterpret_cast<uint4*>(t + e * kCopyThreads * 16) = w[e];
     if (unit == 0)
       for (int e = (int)threadIdx.x; e < c.page_scales; e += kCopyThreads)
         scales[tp * c.page_scales + e] = scales[fp * c.page_scales + e];
@@ -273,7 +272,7 @@ __global__ __launch_bounds__(kCopyThreads) void kv_copy_kernel(KvPagesParams p) 
 
 __global__ __launch_bounds__(kCopyThreads) void kv_fork_kernel(KvPagesParams p) {
   if (!p.plan.head[0]) return;
-  for (int i = (int)blockIdx.x; i < p.n; i += (int)gridDim.x) {
+  for (int i = blockIdx.y == 0 ? (int)blockIdx.x : p.n; i < p.n; i += (int)gridDim.x) {
     const int src = p.a[i], dst = p.b[i], len = p.plan.row[p.rows + i], full = len / kKvPage;
     const int tail = len % kKvPage != 0;
     for (int c = (int)threadIdx.x; c < p.max_pages; c += kCopyThreads) {
@@ -294,7 +293,7 @@ __global__ __launch_bounds__(kCopyThreads) void kv_fork_kernel(KvPagesParams p) 
 
 __global__ __launch_bounds__(kCopyThreads) void kv_resize_kernel(KvPagesParams p) {
   if (!p.plan.head[0]) return;
-  for (int i = (int)blockIdx.x; i < p.rows; i += (int)gridDim.x) {
+  for (int i = blockIdx.y == 0 ? (int)blockIdx.x : p.rows; i < p.rows; i += (int)gridDim.x) {
     const int len = p.lens[i], want = p.a[i] < 0 ? len : p.a[i];
     const int have = (len + kKvPage - 1) / kKvPage, need = (want + kKvPage - 1) / kKvPage;
     int* row = p.table + (int64_t)i * p.max_pages;
@@ -326,7 +325,8 @@ __global__ __launch_bounds__(kCopyThreads) void kv_compact_kernel(KvPagesParams 
   const int moves = p.plan.head[1], live = p.plan.head[2];
   if (moves == 0) return;
   const int64_t entries = (int64_t)p.rows * p.max_pages;
-  const int64_t thread = (int64_t)blockIdx.x * kCopyThreads + threadIdx.x, threads = (int64_t)gridDim.x * kCopyThreads;
+  const int64_t wg = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  const int64_t thread = wg * kCopyThreads + threadIdx.x, threads = (int64_t)gridDim.x * gridDim.y * kCopyThreads;
   for (int64_t i = thread; i < entries; i += threads) {
     const int id = p.table[i];
     if (id >= live && id < p.pool.num_pages) p.table[i] = p.plan.take[id];

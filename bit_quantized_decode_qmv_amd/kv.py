@@ -9,6 +9,7 @@ checks its arguments, allocates what it returns and passes the current stream.
 from __future__ import annotations
 
 import ctypes
+import sys
 from typing import Optional
 
 KV_PAGE = 64
@@ -55,15 +56,50 @@ def declare(lib) -> None:
         fn.argtypes = args
 
 
-def _pkg():
-    import bit_quantized_decode_qmv_amd as bq
-    return bq
+# the package (its library, errors and checks) and torch, which is imported
+# when the first tensor comes
+_bq = sys.modules[__package__]
+_torch = None
+_raw_stream = None
+
+
+def _use_torch():
+    global _torch, _raw_stream
+    import torch
+    # the current stream's handle by itself where torch offers it: a call's
+    # host time is a few microseconds in all
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _torch = torch
+    return torch
+
+
+def _stream(device) -> int:
+    if _raw_stream is not None and device.index is not None:
+        return _raw_stream(device.index)
+    return _bq._stream_handle(device)
+
+
+def _need(t, name, dtype, device) -> None:
+    """A contiguous tensor of dtype on device; what it is not is said by the package's check."""
+    try:
+        if t.dtype is dtype and t.device == device and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    _bq._check(t, name, dtype, device)
+
+
+def _call(name, *args):
+    lib = _bq._lib or _bq.load_library()
+    st = getattr(lib, name)(*args)
+    if st < 0:
+        raise _bq.BQError(st, lib.bq_strerror(st).decode(), name)
+    return st
 
 
 def _c_entry(name):
     def fn(*args):
-        bq = _pkg()
-        return bq._raise_if(getattr(bq.load_library(), name)(*args), name)
+        return _call(name, *args)
     fn.__name__ = name
     fn.__doc__ = f"C entry point {name} of include/bq.h (pointers and stream as integers, the cache as KVCache.desc)."
     return fn
@@ -82,17 +118,14 @@ bq_kv_copy_pages = _c_entry("bq_kv_copy_pages")
 def bq_kv_attn_workspace(desc, q_heads, batch, total):
     """Workspace bytes bq_kv_attn wants for its full split (host only)."""
     n = ctypes.c_size_t(0)
-    bq = _pkg()
-    bq._raise_if(bq.load_library().bq_kv_attn_workspace(desc, q_heads, batch, total, ctypes.byref(n)),
-                 "bq_kv_attn_workspace")
+    _call("bq_kv_attn_workspace", desc, q_heads, batch, total, ctypes.byref(n))
     return n.value
 
 
 def bq_kv_pages_workspace(desc, rows):
     """Workspace bytes the page calls need (host only)."""
     n = ctypes.c_size_t(0)
-    bq = _pkg()
-    bq._raise_if(bq.load_library().bq_kv_pages_workspace(desc, rows, ctypes.byref(n)), "bq_kv_pages_workspace")
+    _call("bq_kv_pages_workspace", desc, rows, ctypes.byref(n))
     return n.value
 
 
@@ -106,15 +139,16 @@ class KVCache:
                  "desc")
 
     def __init__(self, k, v, k_scales, v_scales, format: str = "int8"):
-        bq = _pkg()
-        torch = bq._torch()
+        torch = _torch or _use_torch()
         if format not in KV_FORMATS:
             raise ValueError(f"format must be one of {sorted(KV_FORMATS)}, got {format!r}")
-        bq._check(k, "k", torch.uint8, None)
+        if not isinstance(k, torch.Tensor) or not k.is_cuda:
+            _bq._check(k, "k", torch.uint8, None)
         dev = k.device
-        bq._check(v, "v", torch.uint8, dev)
-        bq._check(k_scales, "k_scales", torch.float32, dev)
-        bq._check(v_scales, "v_scales", torch.float32, dev)
+        _need(k, "k", torch.uint8, dev)
+        _need(v, "v", torch.uint8, dev)
+        _need(k_scales, "k_scales", torch.float32, dev)
+        _need(v_scales, "v_scales", torch.float32, dev)
         shape = k.shape
         if len(shape) != 4 or shape[3] % KV_PAGE:
             raise ValueError(f"k has shape {tuple(shape)}, expected [layers][pages][kv_heads][{KV_PAGE} * head_dim]")
@@ -133,7 +167,7 @@ class KVCache:
     @classmethod
     def empty(cls, layers: int, num_pages: int, kv_heads: int, head_dim: int, format: str = "int8", device="cuda"):
         """A cache of its own memory, uninitialised: tokens exist once they are appended."""
-        torch = _pkg()._torch()
+        torch = _torch or _use_torch()
         codes = (layers, num_pages, kv_heads, KV_PAGE * head_dim)
         scales = (layers, num_pages, kv_heads, KV_PAGE // KV_BLOCK)
         return cls(*(torch.empty(codes, dtype=torch.uint8, device=device) for _ in range(2)),
@@ -142,23 +176,24 @@ class KVCache:
 
 def _rows(t, name, device, heads=None, head_dim=None):
     """Checks a row array [tokens][heads][head_dim], fp16, any row stride; returns its row stride."""
-    torch = _pkg()._torch()
+    torch = _torch or _use_torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be on the GPU, got {t.device}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dtype != torch.float16:
+    if t.dtype is not torch.float16:
         raise TypeError(f"{name} must be torch.float16, got {t.dtype}")
     shape = t.shape
     if len(shape) != 3 or (heads is not None and shape[1] != heads) or (head_dim is not None and shape[2] != head_dim):
         raise ValueError(f"{name} has shape {tuple(shape)}, expected [tokens][{heads or 'heads'}][{head_dim or 'head_dim'}]")
+    n, h, d = shape
     s0, s1, s2 = t.stride()
-    row = shape[1] * shape[2]
-    if s2 != 1 or (s1 != shape[2] and shape[1] > 1):
+    row = h * d
+    if s2 != 1 or (s1 != d and h > 1):
         raise ValueError(f"{name} must hold each row [heads][head_dim] contiguously")
-    if shape[0] <= 1:
+    if n <= 1:
         return row  # a single row has no stride
     if s0 < row:
         raise ValueError(f"{name} has overlapping rows (stride {s0}, row {row})")
@@ -166,11 +201,10 @@ def _rows(t, name, device, heads=None, head_dim=None):
 
 
 def _batch(cu, lens, table, device):
-    bq = _pkg()
-    torch = bq._torch()
-    bq._check(cu, "cu", torch.int32, device)
-    bq._check(lens, "lens", torch.int32, device)
-    bq._check(table, "table", torch.int32, device)
+    i32 = _torch.int32
+    _need(cu, "cu", i32, device)
+    _need(lens, "lens", i32, device)
+    _need(table, "table", i32, device)
     n = lens.shape[0]
     if lens.dim() != 1 or cu.dim() != 1 or cu.shape[0] != n + 1 or table.dim() != 2 or table.shape[0] != n:
         raise ValueError(f"expected lens [batch], cu [batch + 1], table [batch][max_pages]; got {tuple(lens.shape)}, "
@@ -184,28 +218,25 @@ def _angles(pos, inv_freq, axis, adjacent, tokens, device):
         if pos is not None or axis is not None:
             raise ValueError("pos and axis need inv_freq")
         return None, None, None, 0, 1, 0
-    bq = _pkg()
-    torch = bq._torch()
-    bq._check(inv_freq, "inv_freq", torch.float32, device)
-    bq._check(pos, "pos", torch.int32, device)
+    _need(inv_freq, "inv_freq", _torch.float32, device)
+    _need(pos, "pos", _torch.int32, device)
     rot = 2 * inv_freq.numel()
-    if pos.dim() == 1:
-        pos = pos[None]
-    if pos.dim() != 2 or pos.shape[1] != tokens:
+    axes = 1 if pos.dim() == 1 else pos.shape[0]
+    if pos.dim() not in (1, 2) or pos.shape[-1] != tokens:
         raise ValueError(f"pos has shape {tuple(pos.shape)}, expected [axes][{tokens}]")
     if axis is not None:
-        bq._check(axis, "axis", torch.int32, device)
+        _need(axis, "axis", _torch.int32, device)
         if axis.numel() * 2 != rot:
             raise ValueError(f"axis has {axis.numel()} values, inv_freq {inv_freq.numel()}")
-    return (pos.data_ptr(), inv_freq.data_ptr(), axis.data_ptr() if axis is not None else None, rot, pos.shape[0],
+    return (pos.data_ptr(), inv_freq.data_ptr(), axis.data_ptr() if axis is not None else None, rot, axes,
             ROPE_ADJACENT if adjacent else 0)
 
 
 def _out(t, name, like, device):
+    """(tensor, row stride): t checked against the rows of `like`, or new contiguous rows."""
     if t is None:
-        bq = _pkg()
-        t = bq._torch().empty(like.shape, dtype=like.dtype, device=device)
-        return t, like.shape[1] * like.shape[2]
+        shape = like.shape
+        return like.new_empty(shape), shape[1] * shape[2]
     return t, _rows_like(t, name, like, device)
 
 
@@ -222,13 +253,12 @@ def rope(x, pos, inv_freq, axis=None, adjacent: bool = False, out=None):
     r + rot/2; adjacent: 2r and 2r + 1).  pos int32 [axes][tokens] (or
     [tokens]), inv_freq float32, axis int32 (None: the first axis for all).
     out may be x."""
-    bq = _pkg()
     stride = _rows(x, "x", None)
     dev = x.device
     tokens, heads, dim = x.shape
     a = _angles(pos, inv_freq, axis, adjacent, tokens, dev)
     out, out_stride = _out(out, "out", x, dev)
-    bq_rope(x.data_ptr(), out.data_ptr(), stride, out_stride, tokens, heads, dim, *a, bq._stream_handle(dev))
+    _call("bq_rope", x.data_ptr(), out.data_ptr(), stride, out_stride, tokens, heads, dim, *a, _stream(dev))
     return out
 
 
@@ -238,11 +268,10 @@ def kv_append(cache: KVCache, layer: int, k, v, cu, lens, table, q=None, pos=Non
     last tokens of their sequences (lens counts them), k turned as rope()
     does; with q [total][q_heads][head_dim] also returns q turned (into q_out
     when given).  Without inv_freq nothing turns."""
-    bq = _pkg()
     dev = cache.device
-    total = k.shape[0]
     k_stride = _rows(k, "k", dev, cache.kv_heads, cache.head_dim)
     v_stride = _rows_like(v, "v", k, dev)
+    total = k.shape[0]
     batch, max_pages = _batch(cu, lens, table, dev)
     a = _angles(pos, inv_freq, axis, adjacent, total, dev)
     qp = op = None
@@ -253,23 +282,20 @@ def kv_append(cache: KVCache, layer: int, k, v, cu, lens, table, q=None, pos=Non
             raise ValueError(f"q has {q.shape[0]} rows, k {total}")
         q_out, out_stride = _out(q_out, "q_out", q, dev)
         qp, op, q_heads = q.data_ptr(), q_out.data_ptr(), q.shape[1]
-    bq_kv_append(cache.desc, layer, k.data_ptr(), v.data_ptr(), k_stride, v_stride, qp, op, q_stride, out_stride,
-                 q_heads, cu.data_ptr(), lens.data_ptr(), table.data_ptr(), batch, max_pages, total, *a,
-                 bq._stream_handle(dev))
+    _call("bq_kv_append", cache.desc, layer, k.data_ptr(), v.data_ptr(), k_stride, v_stride, qp, op, q_stride,
+          out_stride, q_heads, cu.data_ptr(), lens.data_ptr(), table.data_ptr(), batch, max_pages, total, *a,
+          _stream(dev))
     return q_out if q is not None else None
 
 
 def kv_read(cache: KVCache, layer: int, cu, lens, table, total: int):
     """(k, v) fp16 [total][kv_heads][head_dim]: the values held for the last
     cu[b+1] - cu[b] tokens of each sequence; total = cu[-1]."""
-    bq = _pkg()
-    torch = bq._torch()
     dev = cache.device
     batch, max_pages = _batch(cu, lens, table, dev)
-    k = torch.empty((total, cache.kv_heads, cache.head_dim), dtype=torch.float16, device=dev)
-    v = torch.empty_like(k)
-    bq_kv_read(cache.desc, layer, k.data_ptr(), v.data_ptr(), cu.data_ptr(), lens.data_ptr(), table.data_ptr(), batch,
-               max_pages, total, bq._stream_handle(dev))
+    k, v = (_torch.empty((total, cache.kv_heads, cache.head_dim), dtype=_torch.float16, device=dev) for _ in range(2))
+    _call("bq_kv_read", cache.desc, layer, k.data_ptr(), v.data_ptr(), cu.data_ptr(), lens.data_ptr(),
+          table.data_ptr(), batch, max_pages, total, _stream(dev))
     return k, v
 
 
@@ -281,87 +307,95 @@ def kv_attn(cache: KVCache, layer: int, q, cu, lens, table, scale: Optional[floa
     last `window` of them; else every token held.  workspace: a uint8 tensor,
     zero before its first use and kept for later calls (see
     bq_kv_attn_workspace); allocated here when None."""
-    bq = _pkg()
     dev = cache.device
     stride = _rows(q, "q", dev, None, cache.head_dim)
     total, heads, dim = q.shape
     batch, max_pages = _batch(cu, lens, table, dev)
     out, out_stride = _out(out, "out", q, dev)
+    ws, ws_bytes = None, 0
     if workspace is None:
-        torch = bq._torch()
-        need = bq_kv_attn_workspace(cache.desc, heads, batch, total)
-        workspace = torch.zeros(need, dtype=torch.uint8, device=dev) if need else None
+        ws_bytes = bq_kv_attn_workspace(cache.desc, heads, batch, total)
+        workspace = _torch.zeros(ws_bytes, dtype=_torch.uint8, device=dev) if ws_bytes else None
     else:
-        bq._check(workspace, "workspace", bq._torch().uint8, dev)
-    bq_kv_attn(cache.desc, layer, q.data_ptr(), out.data_ptr(), stride, out_stride, heads, cu.data_ptr(),
-               lens.data_ptr(), table.data_ptr(), batch, max_pages, total, dim ** -0.5 if scale is None else scale,
-               window, KV_CAUSAL if causal else 0, workspace.data_ptr() if workspace is not None else None,
-               workspace.numel() if workspace is not None else 0, bq._stream_handle(dev))
+        _need(workspace, "workspace", _torch.uint8, dev)
+        ws_bytes = workspace.numel()
+    if workspace is not None:
+        ws = workspace.data_ptr()
+    _call("bq_kv_attn", cache.desc, layer, q.data_ptr(), out.data_ptr(), stride, out_stride, heads, cu.data_ptr(),
+          lens.data_ptr(), table.data_ptr(), batch, max_pages, total, dim ** -0.5 if scale is None else scale, window,
+          KV_CAUSAL if causal else 0, ws, ws_bytes, _stream(dev))
     return out
 
 
-def _ints(t, name, device, shape):
-    bq = _pkg()
-    bq._check(t, name, bq._torch().int32, device)
+def _ints(t, name, device, *shape):
+    _need(t, name, _torch.int32, device)
     if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
 
 
-def _page_call(name, cache, table, refs, workspace, *args):
-    """args: the tensors and sizes between rows, max_pages and status."""
-    bq = _pkg()
-    torch = bq._torch()
+def _page_call(name, cache, table, refs, workspace, before, after):
+    """before, after: the pointers and sizes ahead of refs and behind max_pages."""
     dev = cache.device
-    bq._check(table, "table", torch.int32, dev)
+    _ints(refs, "refs", dev, cache.num_pages)
+    rows, max_pages = table.shape
+    status = _torch.empty(2, dtype=_torch.int32, device=dev)
+    if workspace is None:
+        size = bq_kv_pages_workspace(cache.desc, rows)
+        workspace = _torch.empty(size, dtype=_torch.uint8, device=dev)
+    else:
+        _need(workspace, "workspace", _torch.uint8, dev)
+        size = workspace.numel()
+    _call(name, cache.desc, table.data_ptr(), *before, refs.data_ptr(), rows, max_pages, *after, status.data_ptr(),
+          workspace.data_ptr(), size, _stream(dev))
+    return status
+
+
+def _table(table, device):
+    _need(table, "table", _torch.int32, device)
     if table.dim() != 2:
         raise ValueError(f"table has shape {tuple(table.shape)}, expected [rows][max_pages]")
-    _ints(refs, "refs", dev, (cache.num_pages,))
-    status = torch.empty(2, dtype=torch.int32, device=dev)
-    if workspace is None:
-        workspace = torch.empty(bq_kv_pages_workspace(cache.desc, table.shape[0]), dtype=torch.uint8, device=dev)
-    else:
-        bq._check(workspace, "workspace", torch.uint8, dev)
-    lens, *rest = args
-    bq._raise_if(getattr(bq.load_library(), name)(
-        cache.desc, table.data_ptr(), *([lens.data_ptr()] if lens is not None else []), refs.data_ptr(),
-        table.shape[0], table.shape[1], *rest, status.data_ptr(), workspace.data_ptr(), workspace.numel(),
-        bq._stream_handle(dev)), name)
-    return status
+    return table.shape[0]
 
 
 def kv_fork(cache: KVCache, table, lens, refs, src, dst, workspace=None):
     """Row dst[i] becomes a copy of row src[i]: whole pages shared, a partly
     filled last page copied.  Updates table, lens, refs on the GPU and
     returns status int32 [2] (0 / -1 invalid / pages short; pages copied)."""
-    _ints(lens, "lens", cache.device, table.shape[:1])
+    dev = cache.device
+    rows = _table(table, dev)
+    _ints(lens, "lens", dev, rows)
     n = src.shape[0]
-    _ints(src, "src", cache.device, (n,))
-    _ints(dst, "dst", cache.device, (n,))
-    return _page_call("bq_kv_fork", cache, table, refs, workspace, lens, src.data_ptr(), dst.data_ptr(), n)
+    _ints(src, "src", dev, n)
+    _ints(dst, "dst", dev, n)
+    return _page_call("bq_kv_fork", cache, table, refs, workspace, (lens.data_ptr(),),
+                      (src.data_ptr(), dst.data_ptr(), n))
 
 
 def kv_resize(cache: KVCache, table, lens, refs, want, workspace=None):
     """Row i gets the length want[i] (-1: as it is): pages are let go or
     taken, a shared page that becomes the partly filled last one is copied.
     Returns status as kv_fork."""
-    _ints(lens, "lens", cache.device, table.shape[:1])
-    _ints(want, "want", cache.device, table.shape[:1])
-    return _page_call("bq_kv_resize", cache, table, refs, workspace, lens, want.data_ptr())
+    dev = cache.device
+    rows = _table(table, dev)
+    _ints(lens, "lens", dev, rows)
+    _ints(want, "want", dev, rows)
+    return _page_call("bq_kv_resize", cache, table, refs, workspace, (lens.data_ptr(),), (want.data_ptr(),))
 
 
 def kv_compact(cache: KVCache, table, refs, workspace=None):
     """Moves pages so that those in use have the lowest ids; table and refs
     follow.  Returns status as kv_fork (status[1]: pages moved)."""
-    return _page_call("bq_kv_compact", cache, table, refs, workspace, None)
+    _table(table, cache.device)
+    return _page_call("bq_kv_compact", cache, table, refs, workspace, (), ())
 
 
 def kv_copy_pages(cache: KVCache, src, dst) -> None:
     """Copies pages src[i] to dst[i] over all layers."""
-    bq = _pkg()
+    dev = cache.device
     n = src.shape[0]
-    _ints(src, "src", cache.device, (n,))
-    _ints(dst, "dst", cache.device, (n,))
-    bq_kv_copy_pages(cache.desc, src.data_ptr(), dst.data_ptr(), n, bq._stream_handle(cache.device))
+    _ints(src, "src", dev, n)
+    _ints(dst, "dst", dev, n)
+    _call("bq_kv_copy_pages", cache.desc, src.data_ptr(), dst.data_ptr(), n, _stream(dev))
 
 
 __all__ = [

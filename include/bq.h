@@ -326,8 +326,8 @@ int bq_spec_decode_verify_noalloc(const void* logits, int logits_dtype, const in
  * them:
  *   K  [i: 4][c: head_dim/64][g: 4][t: 16][j: 16]  token 16i + t, dim 64c + 16g + j
  *   V  [n: head_dim/16][g: 4][d: 16][i: 4][j: 4]   token 16i + 4g + j, dim 16n + d
- * head_dim 64, 128, 192 or 256; kv_heads 1..1024; codes and scales 16-byte
- * aligned.  layer selects one layer of the arrays; page calls work on all.
+ * head_dim 64, 128, 192 or 256; kv_heads 1..1024; layers 1..4096; scales are
+ * not negative; codes and scales 16-byte aligned.  layer selects one layer of the arrays; page calls work on all.
  *
  * The batch of a call.  Sequence b has the rows cu[b] .. cu[b+1] - 1 of the
  * call's packed row arrays (cu: int32 [batch + 1], rising, cu[batch] =
