@@ -24,9 +24,9 @@ KvPool pool_of(const bq_kv_cache* c) {
 // one pair each, up to sixteen for each CU, from where on they take several
 // pairs.
 dim3 copy_grid(const KvPool& p, int64_t most) {
-  const int64_t units = (p.page_bytes + kCopyUnit - 1) / kCopyUnit;
+  const int64_t units = p.page_bytes / kCopyUnit;
   const int64_t pairs = std::clamp<int64_t>(4096 / (units * p.layers * 2), 1, std::max<int64_t>(most, 1));
-  return dim3((unsigned)(units * pairs), (unsigned)(p.layers * 2));
+  return dim3((unsigned)(p.layers * 2), (unsigned)(units * pairs));
 }
 
 int check_tables(const bq_kv_cache* cache, const int* table, const int* refs, int rows, int max_pages, const int* status,

@@ -129,6 +129,10 @@ def bq_kv_pages_workspace(desc, rows):
     return n.value
 
 
+# bq_kv_pages_workspace by (pages, rows), of which alone it is a function
+_pages_bytes = {}
+
+
 class KVCache:
     """A paged key/value cache in 8 bits over the caller's tensors:
     k, v uint8 [layers][pages][kv_heads][64 * head_dim], k_scales, v_scales
@@ -340,7 +344,9 @@ def _page_call(name, cache, table, refs, workspace, before, after):
     rows, max_pages = table.shape
     status = _torch.empty(2, dtype=_torch.int32, device=dev)
     if workspace is None:
-        size = bq_kv_pages_workspace(cache.desc, rows)
+        size = _pages_bytes.get((cache.num_pages, rows))
+        if size is None:
+            size = _pages_bytes[cache.num_pages, rows] = bq_kv_pages_workspace(cache.desc, rows)
         workspace = _torch.empty(size, dtype=_torch.uint8, device=dev)
     else:
         _need(workspace, "workspace", _torch.uint8, dev)
