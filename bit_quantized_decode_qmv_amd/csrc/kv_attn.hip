@@ -77,8 +77,20 @@ int check_attn(const bq_kv_cache* cache, int q_heads, int batch, int total) {
   if (st != BQ_OK) return st;
   if (q_heads < 1 || q_heads > 65536 || q_heads % cache->kv_heads != 0) return BQ_ERR_SHAPE;
   if (batch < 1 || batch > (1 << 20) || total < 0 || total > (1 << 28) ||
-      (int64_t)total * (q_heads / cache->kv_heads) > 0x7FFFFFFF)
+      (int64_t)total * (q_heads / cache->kv_heads) > 0x7FFFFF00)
     return BQ_ERR_SHAPE;
+  return BQ_OK;
+}
+
+// The launches of `wgs` shares of each head; a grid's y holds 65535 at most.
+int launch_shares(const void* fn, int64_t wgs, int threads, KvAttnParams& p, void* stream) {
+  constexpr int64_t kMost = 32768;
+  for (int64_t at = 0; at < wgs; at += kMost) {
+    p.item0 = (int)at;
+    const int st = kv_launch(fn, dim3((unsigned)p.kv_heads, (unsigned)std::min(kMost, wgs - at)), dim3((unsigned)threads), 0,
+                             stream, &p);
+    if (st != BQ_OK) return st;
+  }
   return BQ_OK;
 }
 
@@ -135,13 +147,11 @@ int bq_kv_attn(const bq_kv_cache* cache, int layer, const void* q, void* out, lo
   p.counters = static_cast<unsigned*>(workspace);
   p.part = workspace ? reinterpret_cast<float*>(static_cast<char*>(workspace) + BQ_KV_ATTN_COUNTER_BYTES) : nullptr;
   const int64_t wgs = pl.tiles + pl.target;
-  if (wgs * 16 > 0x7FFFFFFF) return BQ_ERR_SHAPE;
   if (pl.rows < kPromptRows)
-    return kv_launch(pick_rows(D, pl.rows, cache->format), dim3((unsigned)cache->kv_heads, (unsigned)wgs),
-                     dim3((unsigned)(64 * kv_waves(D))), 0, stream, &p);
-  st = kv_launch(pick_prompt(D, cache->format), dim3((unsigned)cache->kv_heads, (unsigned)wgs), dim3(kPromptThreads), 0,
-                 stream, &p);
+    return launch_shares(pick_rows(D, pl.rows, cache->format), wgs, 64 * kv_waves(D), p, stream);
+  st = launch_shares(pick_prompt(D, cache->format), wgs, kPromptThreads, p, stream);
   if (st != BQ_OK || pl.target == 0) return st;
+  // (tiles that are split are fewer than the workgroups to aim at)
   const int64_t joined = pl.tiles * (kPromptRows / 16);
   return kv_launch(pick_join(D), dim3((unsigned)cache->kv_heads, (unsigned)joined), dim3(256), 0, stream, &p);
 }

@@ -30,6 +30,7 @@ struct KvAttnParams {
   float* part;           // workspace: partial results
   int target;            // workgroups of a head to aim at; 0: tiles are not split
   int min_pages;         // of a part; 0: by the number of pages
+  int item0;             // share of the launch's first workgroups
 };
 
 constexpr int kKvMaxParts = 128;  // of a tile
@@ -96,16 +97,23 @@ __device__ __forceinline__ bool kv_attn_work(const KvAttnParams& p, int item, Kv
     return max((s.len + kKvPage - 1) / kKvPage - kv_first_page(p, s), 1);
   };
   const auto tiles = [&](const KvSeq& s) { return (s.n * p.group + ROWS - 1) / ROWS; };
-  const KvSeq first = lane < batch ? kv_seq(p.batch, lane) : KvSeq{};
-  const auto seq = [&](int base) {
-    return base == 0 ? first : base + lane < batch ? kv_seq(p.batch, base + lane) : KvSeq{};
+  // Offsets that fall would make the list longer than the launch and the
+  // workspace are made for: then there is no work.
+  bool falls = false;
+  const auto load = [&](int b) {
+    if (b >= batch) return KvSeq{};
+    falls = falls || p.batch.cu[b + 1] < p.batch.cu[b];
+    return kv_seq(p.batch, b);
   };
+  const KvSeq first = load(lane);
+  const auto seq = [&](int base) { return base == 0 ? first : load(base + lane); };
   w.chunk = 0x7FFFFFFF;
   if (p.target > 0) {
     // the batch's tiles times pages over the target: a long sequence gets as
     // many more parts as it has more pages
     int all = 0;
     for (int base = 0; base < batch; base += 64) all += tiles(seq(base)) * pages(seq(base));
+    if (__ballot(falls) != 0) return false;
     all = __builtin_amdgcn_readlane(kv_scan(all), 63);
     // few rows: no part shorter than pays for joining it (measured, one
     // sequence, 8 heads of 128: 16 pages 10.0 us in one part and 11.9 in two;
@@ -152,6 +160,7 @@ __device__ __forceinline__ bool kv_attn_work(const KvAttnParams& p, int item, Kv
   int before_tiles = 0, before_wholes = 0;
   for (int base = 0; base < batch; base += 64) {
     const KvSeq s = seq(base);
+    if (__ballot(falls) != 0) return false;
     const int nt = tiles(s), nw = p.target > 0 ? nt * whole(s) : 0;
     const int st = kv_scan(nt), sw = p.target > 0 ? kv_scan(nw) : 0;
     const int mine = item - wholes - before_tiles, all_t = __builtin_amdgcn_readlane(st, 63);
@@ -238,7 +247,7 @@ __global__ __launch_bounds__(64 * kv_waves(D)) void kv_attn_rows_kernel(KvAttnPa
   __shared__ int last;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int lane = (int)threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-  const int item = (int)blockIdx.y, head = (int)blockIdx.x;
+  const int item = p.item0 + (int)blockIdx.y, head = (int)blockIdx.x;
   KvWork w;
   if (!kv_attn_work<ROWS>(p, item, w)) return;
   const KvSeq s = w.s;

@@ -209,6 +209,7 @@ inline bool kv_rows_ok(const void* p, long long stride, int row) {
 }
 
 inline int kv_launch(const void* fn, dim3 grid, dim3 block, size_t shmem, void* stream, void* params) {
+  if ((uint64_t)grid.x * block.x > 0xFFFFFFFFu || grid.y > 65535) return BQ_ERR_SHAPE;
   void* args[] = {params};
   return hipLaunchKernel(fn, grid, block, args, shmem, static_cast<hipStream_t>(stream)) == hipSuccess ? BQ_OK
                                                                                                        : BQ_ERR_HIP;

@@ -47,7 +47,7 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
   const int lane = (int)threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int head = (int)blockIdx.x;
-  const int item = (int)blockIdx.y;
+  const int item = p.item0 + (int)blockIdx.y;
   KvWork w;
   if (!kv_attn_work<kPromptRows>(p, item, w)) return;
   const KvSeq s = w.s;

@@ -70,15 +70,14 @@ def rope_f64(x, pos, inv_freq, axis=None, adjacent=False):
 def kv_sequence(cache, layer, row, n, which):
     """Held values [n][heads][D] of a table row's first n tokens, fp64."""
     D = cache["k"].shape[3] // PAGE
-    codes = kv_table(cache["format"])[cache[which][layer]][:, :, kv_places(which, D).ravel()]
+    ids = np.asarray(row[:-(-n // PAGE)], dtype=np.int64)
+    held = (ids >= 0) & (ids < cache["k"].shape[1])
+    ids = np.where(held, ids, 0)
+    codes = kv_table(cache["format"])[cache[which][layer][ids]][:, :, kv_places(which, D).ravel()]
     codes = codes.reshape(codes.shape[0], codes.shape[1], PAGE, D)
-    values = codes * np.repeat(cache[which + "s"][layer].astype(np.float64), BLOCK, axis=-1)[..., None]
-    out = np.zeros((n, values.shape[1], D))
-    for t in range(n):
-        p = int(row[t // PAGE])
-        if 0 <= p < values.shape[0]:
-            out[t] = values[p, :, t % PAGE]
-    return out
+    values = codes * np.repeat(cache[which + "s"][layer][ids].astype(np.float64), BLOCK, axis=-1)[..., None]
+    # [pages][heads][64][D] to tokens; a page that is none holds nothing
+    return np.where(held[:, None, None, None], values, 0.0).swapaxes(1, 2).reshape(-1, values.shape[1], D)[:n]
 
 
 def kv_append_f64(cache, layer, row, start, k, v):
