@@ -4,8 +4,8 @@
 // over the tokens j that row r sees.  k_j = sk * code with sk constant over a
 // block of 16 tokens, so the scale is taken out of the dot product; likewise
 // p_j v_j = (p_j sv) * code.  Codes enter the matrix cores as fp16, exactly;
-// scores, probabilities' sums and outputs are held in fp32; the probabilities
-// are rounded to fp16 (nearest even) for the second product.
+// scores, probabilities' sums and outputs are held in fp32; how the
+// probabilities enter the second product is said at each kernel.
 //
 // The `group` query heads that share a key/value head and the tokens of a
 // sequence's rows form one list of rows (token-major), taken 16 at a time as
@@ -51,6 +51,16 @@ __device__ __forceinline__ float kv_max3(float a, float b, float c) {
   float d;
   asm("v_max3_f32 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "v"(c));  // (without quieting each operand first)
   return d;
+}
+// The larger of each half (fp16, not negative) of three dwords; a half that
+// is no number stays so.
+__device__ __forceinline__ uint32_t kv_pk_max3(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("v_pk_maximum3_f16 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "v"(c));
+  return d;
+}
+__device__ __forceinline__ float kv_min4(f32x4 x) {
+  return __builtin_fminf(__builtin_fminf(x[0], x[1]), __builtin_fminf(x[2], x[3]));
 }
 // R becomes the power of two above the scale rmax, invR its reciprocal; what
 // values in units of the old one are multiplied by.
@@ -213,6 +223,26 @@ struct KvPages {
   }
 };
 
+// The offset of the codes of K, in a row's scores.
+template <bool BYTES, int COUNT>
+__device__ __forceinline__ float kv_query_offset(const half8_t (&q)[COUNT]) {
+  if constexpr (!BYTES) return 0.f;
+  float sum = 0.f;
+#pragma unroll
+  for (int c = 0; c < COUNT; ++c)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum += (float)q[c][j];
+  return -kKvOffset<BYTES> * kv_col_sum(sum);
+}
+// The offset of the codes of V as rows of an operand.
+template <bool BYTES>
+__device__ __forceinline__ half8_t kv_offset_operand() {
+  half8_t v;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = (_Float16)kKvOffset<BYTES>;
+  return v;
+}
+
 // One page's codes in flight or at hand, as a wave holds them.
 template <int D>
 struct KvCodes {
@@ -239,9 +269,15 @@ constexpr int kv_waves(int D) { return D <= 128 ? 8 : 4; }
 // probabilities, at most 2^8, stay well inside fp16.  They are taken as the
 // sum of two fp16 numbers, so that no more than 2^-22 of a probability is
 // lost: the second product is cheap beside the loads.
+//
+// Measured, 8 heads of 128 with 6 query heads each: one row over 131001
+// tokens 55 us (4.9 TB/s of codes), over 1003 tokens 9.6 us (a launch, the
+// table, one page a wave and the join); five rows each of 32 sequences of
+// 1024 to 16384 tokens (e4m3) 82 us (4.6 TB/s).
 template <int D, int FMT, int RT>
 __global__ __launch_bounds__(64 * kv_waves(D)) void kv_attn_rows_kernel(KvAttnParams p) {
   constexpr int C = D / 64, N = D / 16, ROWS = 16 * RT, NW = kv_waves(D), THREADS = 64 * NW;
+  constexpr bool BYTES = FMT == BQ_KV_I8;
   constexpr int JOIN = NW * (N * 256 + 32);
   __shared__ __align__(16) float lds[JOIN > 2 * kKvMaxParts * ROWS ? JOIN : 2 * kKvMaxParts * ROWS];
   __shared__ int last;
@@ -267,6 +303,7 @@ __global__ __launch_bounds__(64 * kv_waves(D)) void kv_attn_rows_kernel(KvAttnPa
     const int page = pages_of.at(p, w.b, begin + wave, NW, end, k);
     return page < 0 ? -1 : (int64_t)page * p.kv_heads + head;
   };
+  const float scale = p.scale * kKvUnit<BYTES>;
   KvCodes<D> x;
   const auto load_k = [&](int64_t at) {
     const kv_rsrc_t rs = kv_rsrc(p.k + max(at, (int64_t)0) * (kKvPage * D), at < 0 ? 0 : kKvPage * D);
@@ -306,13 +343,20 @@ __global__ __launch_bounds__(64 * kv_waves(D)) void kv_attn_rows_kernel(KvAttnPa
       q[t][c] = ok ? *reinterpret_cast<const half8_t*>(src + (c >> 1) * 64 + (c & 1) * 8) : half8_t{};
   }
 
-  f32x4 o[RT][N];
+  // what the offset of the codes adds to every score of a row
+  float q_off[RT];
+#pragma unroll
+  for (int t = 0; t < RT; ++t) q_off[t] = kv_query_offset<BYTES>(q[t]);
+  const half8_t ones = kv_offset_operand<BYTES>();
+
+  f32x4 o[RT][N], o_off[RT];  // o_off: what the codes' offset adds to each o
   float m[RT], l[RT];
   float R = 0x1p-100f, invR = 0x1p100f;  // o is in units of R, a power of two near the largest scale of V so far
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
     m[t] = -__builtin_inff();
     l[t] = 0.f;
+    o_off[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int n = 0; n < N; ++n) o[t][n] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
@@ -330,7 +374,7 @@ __global__ __launch_bounds__(64 * kv_waves(D)) void kv_attn_rows_kernel(KvAttnPa
       for (int t = 0; t < RT; ++t) y[t][i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const half8_t a0 = kv_half8<FMT>(x.k[i][c][0], x.k[i][c][1]), a1 = kv_half8<FMT>(x.k[i][c][2], x.k[i][c][3]);
+        const half8_t a0 = kv_operand8<FMT, BYTES>(x.k[i][c][0], x.k[i][c][1]), a1 = kv_operand8<FMT, BYTES>(x.k[i][c][2], x.k[i][c][3]);
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
           y[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a0, q[t][2 * c], y[t][i], 0, 0, 0);
@@ -341,7 +385,11 @@ __global__ __launch_bounds__(64 * kv_waves(D)) void kv_attn_rows_kernel(KvAttnPa
 #pragma unroll
     for (int t = 0; t < RT; ++t)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y[t][i] *= sk[i] * p.scale;
+      for (int i = 0; i < 4; ++i) {
+        const float c = sk[i] * scale, off = q_off[t] * c;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[t][i][e] = BYTES ? __builtin_fmaf(y[t][i][e], c, off) : y[t][i][e] * c;
+      }
     load_k(next);
     if (left < kKvPage || j0 + kKvPage > r0.hi || j0 < r1.lo) {
       // a page that some row does not see whole: the row's tokens [lo, hi)
@@ -393,6 +441,7 @@ __global__ __launch_bounds__(64 * kv_waves(D)) void kv_attn_rows_kernel(KvAttnPa
         const float alpha = mn == -__builtin_inff() ? 1.f : kv_exp2(m[t] - mn);
         m[t] = mn;
         l[t] *= alpha;
+        o_off[t] *= alpha * change;
 #pragma unroll
         for (int n = 0; n < N; ++n) o[t][n] *= alpha * change;
       }
@@ -419,13 +468,22 @@ __global__ __launch_bounds__(64 * kv_waves(D)) void kv_attn_rows_kernel(KvAttnPa
     for (int n = 0; n < N; ++n)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const half8_t a = kv_half8<FMT>(x.v[n][2 * h], x.v[n][2 * h + 1]);
+        const half8_t a = kv_operand8<FMT, BYTES>(x.v[n][2 * h], x.v[n][2 * h + 1]);
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
           o[t][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, ph_[t][h], o[t][n], 0, 0, 0);
           o[t][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pl_[t][h], o[t][n], 0, 0, 0);
         }
       }
+    if constexpr (BYTES) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+          o_off[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, ph_[t][h], o_off[t], 0, 0, 0);
+          o_off[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, pl_[t][h], o_off[t], 0, 0, 0);
+        }
+    }
     load_v(next);
     here = next;
   }
@@ -439,7 +497,7 @@ __global__ __launch_bounds__(64 * kv_waves(D)) void kv_attn_rows_kernel(KvAttnPa
   for (int t = 0; t < RT; ++t) {
     const float sum = kv_col_sum(l[t]);
 #pragma unroll
-    for (int n = 0; n < N; ++n) *reinterpret_cast<f32x4*>(lds + ((wave * N + n) * 64 + lane) * 4) = o[t][n] * R;
+    for (int n = 0; n < N; ++n) *reinterpret_cast<f32x4*>(lds + ((wave * N + n) * 64 + lane) * 4) = (o[t][n] - o_off[t]) * (R * kKvUnit<BYTES>);
     if (g == 0) *reinterpret_cast<float2*>(ml + (wave * 16 + r) * 2) = make_float2(m[t], sum);
     __syncthreads();
     const int row = 16 * t + r;  // of the tile; the same for all that a thread takes

@@ -61,6 +61,26 @@ __device__ __forceinline__ half8_t kv_half8(uint32_t a, uint32_t b) {
   return half8_t{x0.x, x0.y, x1.x, x1.y, y0.x, y0.y, y1.x, y1.y};
 }
 
+// Codes as operands of the matrix cores.  BYTES: the byte of an int8 code,
+// code + 128, is as it stands the fp16 subnormal (code + 128) 2^-24, which the
+// matrix cores take exactly; the product with 128 2^-24 is taken off the sums.
+// That is two byte permutes for four codes, where the codes themselves cost
+// two additions more.
+template <bool BYTES>
+constexpr float kKvOffset = BYTES ? 0x1p-17f : 0.f;
+template <bool BYTES>
+constexpr float kKvUnit = BYTES ? 0x1p24f : 1.f;  // of the sums
+template <int FMT, bool BYTES>
+__device__ __forceinline__ half8_t kv_operand8(uint32_t a, uint32_t b) {
+  if constexpr (BYTES) {
+    const u32x4_t w = {__builtin_amdgcn_perm(0u, a, 0x0C010C00u), __builtin_amdgcn_perm(0u, a, 0x0C030C02u),
+                       __builtin_amdgcn_perm(0u, b, 0x0C010C00u), __builtin_amdgcn_perm(0u, b, 0x0C030C02u)};
+    return __builtin_bit_cast(half8_t, w);
+  } else {
+    return kv_half8<FMT>(a, b);
+  }
+}
+
 // One code's value.
 __device__ __forceinline__ float kv_value(int format, uint32_t byte) {
   if (format == BQ_KV_I8) return (float)((int)byte - 128);

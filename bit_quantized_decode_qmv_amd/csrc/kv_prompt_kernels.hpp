@@ -2,8 +2,7 @@
 // whole prompt, or queries over an encoder's states.
 //
 // The same products as for few rows (S^T = K Q^T, O^T += V^T P^T, 32 rows a
-// wave), bound by the matrix cores and, about equally, by the vector units'
-// softmax.  What differs is the sharing: a workgroup's four waves take 128
+// wave).  What differs is the sharing: a workgroup's four waves take 128
 // rows and walk the pages together, so that a page's codes are read and
 // turned into fp16 once for all of them.  The fp16 operands go through LDS in
 // the order in which the waves read them back (16 bytes a lane, consecutive:
@@ -15,6 +14,15 @@
 // scale folded in: 2^-12 of each on average, as the rounding of the result.
 // Their sum is taken of the rounded ones, so that a row that sees few tokens
 // does not keep the rounding of a common factor.
+//
+// Bound by issue: a wave's page of 128 dimensions is 68 matrix instructions
+// (1090 cycles), some 210 vector instructions (1290, a quarter of them for
+// the exponentials) and 32 reads of LDS (256 of the CU's), of two waves a
+// SIMD.  Measured: 2047 rows of 48 heads (8 of them keys' and values') of 128
+// over 10240 tokens 484 us, 0.96 PFLOP/s; the matrix instructions alone 200,
+// without the softmax 334.  One wave a SIMD with 64 rows reads LDS half as
+// often, and took 714 us; eight waves with 256 rows 474 before other steps,
+// but 10 to 40% more where prompts are short.
 #pragma once
 
 #include "kv_attn_kernels.hpp"
@@ -24,10 +32,12 @@ namespace bq {
 // The order of a product whose operands come from LDS: AHEAD reads first,
 // then one more after the two matrix instructions that share one, so that
 // none waits for the read just issued.
-template <int READS>
+// `more` matrix instructions that need none of the reads come first.
+template <int READS, int MORE = 0>
 __device__ __forceinline__ void kv_order_reads() {
   constexpr int AHEAD = READS < 16 ? READS / 2 : 8;
   __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);  // LDS reads
+  if constexpr (MORE > 0) __builtin_amdgcn_sched_group_barrier(0x008, MORE, 0);
 #pragma unroll
   for (int i = 0; i < READS - AHEAD; ++i) {
     __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);  // matrix instructions
@@ -36,12 +46,25 @@ __device__ __forceinline__ void kv_order_reads() {
   __builtin_amdgcn_sched_group_barrier(0x008, 2 * AHEAD, 0);
 }
 
+// Wide heads, whose registers are two files: o stays in the accumulation
+// registers and the scores (ACC false) in the others.  What only a rarely
+// taken branch changes is otherwise copied to and fro on every page, and
+// spills (head_dim 256, 500 rows over 4000 tokens: 124 us and 90).
+template <int D, bool ACC = true>
+__device__ __forceinline__ void kv_stay(f32x4& x) {
+  if constexpr (D > 128) {
+    if constexpr (ACC) asm volatile("" : "+a"(x));
+    else asm volatile("" : "+v"(x));
+  }
+}
+
 constexpr int kPromptWaves = 4, kPromptThreads = 64 * kPromptWaves;
 constexpr int kPromptRows = 32 * kPromptWaves;
 
 template <int D, int FMT>
 __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prompt_kernel(KvAttnParams p) {
   constexpr int C = D / 64, N = D / 16, UNITS = 4 * D / kPromptThreads;  // 16-byte units of K (or V) a thread
+  constexpr bool BYTES = FMT == BQ_KV_I8;
   // [buffer][K, V][operand][lane][8]
   __shared__ __align__(16) half8_t lds[2][2][8 * C][64];
   const int lane = (int)threadIdx.x & 63, r = lane & 15, g = lane >> 4;
@@ -93,8 +116,8 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
       }
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        lds[to][x][2 * op][ln] = kv_half8<FMT>(raw[x][j][0], raw[x][j][1]);
-        lds[to][x][2 * op + 1][ln] = kv_half8<FMT>(raw[x][j][2], raw[x][j][3]);
+        lds[to][x][2 * op][ln] = kv_operand8<FMT, BYTES>(raw[x][j][0], raw[x][j][1]);
+        lds[to][x][2 * op + 1][ln] = kv_operand8<FMT, BYTES>(raw[x][j][2], raw[x][j][3]);
       }
     }
   };
@@ -131,15 +154,30 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
       if (p.scale < 0.f) q[t][c] = -q[t][c];
     }
   }
-  const float scale = __builtin_fabsf(p.scale);
+  const float scale = __builtin_fabsf(p.scale) * kKvUnit<BYTES>;
+  f32x4 q_off[2];  // what the offset of the codes adds to every score: where the sums begin
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const float off = kv_query_offset<BYTES>(q[t]);
+    q_off[t] = f32x4{off, off, off, off};
+  }
 
   f32x4 o[2][N];
-  float m[2], l[2];
+  // Sums over the rounded probabilities, by the matrix cores: rows 4g + e of
+  // one more operand hold, e = 0, V's code offset and, 1 and 2, the two fp16
+  // terms of what takes V's scale out again.
+  f32x4 sums[2];
+  const int term = lane & 3;
+  const float pick_all = term == 2 ? 1.f : 0.f, pick_hi = term == 1 ? 1.f : term == 2 ? -1.f : 0.f;
+  const float pick_off = term == 0 ? kKvOffset<BYTES> : 0.f;
+  float m[2], l[2], base[2];  // base: the maximum that is taken off, 0 while there is none
+  bool fresh = true;          // some row has seen nothing yet
   float R = 0x1p-100f, invR = 0x1p100f;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    m[t] = -__builtin_inff();
-    l[t] = 0.f;
+    m[t] = row0 + 32 * wave + 16 * t + r < rows ? -__builtin_inff() : 0.f;
+    l[t] = base[t] = 0.f;
+    sums[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int n = 0; n < N; ++n) o[t][n] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
@@ -148,6 +186,10 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
   __syncthreads();
   for (int at = begin; at < end; ++at) {
     const int buf = (at - begin) & 1;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int n = 0; n < N; ++n) kv_stay<D>(o[t][n]);
     const int64_t next = place(at + 1 - begin);
     const f32x4 sk = sk_next;
     f32x4 sv = sv_next;
@@ -158,7 +200,8 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
       f32x4 y[2][4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        y[0][i] = y[1][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        y[0][i] = q_off[0];
+        y[1][i] = q_off[1];
 #pragma unroll
         for (int c = 0; c < 2 * C; ++c) {
           const half8_t a = lds[buf][0][2 * C * i + c][lane];
@@ -167,16 +210,20 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
         }
       }
       kv_order_reads<8 * C>();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) kv_stay<D, false>(y[0][i]), kv_stay<D, false>(y[1][i]);
       f32x4 c = sk * scale;
       if (left < kKvPage || j0 + kKvPage > all_hi || j0 < all_lo) {
         // a page that some row does not see whole; a block past the length
         // has no scale (its probabilities are 0 under any)
-        if (left < kKvPage) {
+        int held = left;
+        asm volatile("" : "+s"(held));  // stays in this branch
+        if (held < kKvPage) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (16 * i >= left) {
+            if (16 * i >= held) {
               c[i] = 0.f;
-              sv[i] = left > 0 ? sv[0] : 0.f;
+              sv[i] = held > 0 ? sv[0] : 0.f;
             }
         }
 #pragma unroll
@@ -192,65 +239,87 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
         }
         c = f32x4{1.f, 1.f, 1.f, 1.f};  // a hidden score times 0 would be no number
       }
-      const float rmax = __builtin_fmaxf(__builtin_fmaxf(sv[0], sv[1]), __builtin_fmaxf(sv[2], sv[3]));
-      float mx[2];
-      bool raise = rmax > R;
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        mx[t] = -__builtin_inff();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float top = kv_max3(kv_max3(y[t][i][0], y[t][i][1], y[t][i][2]), y[t][i][3], y[t][i][3]);
-          mx[t] = __builtin_fmaxf(mx[t], top * c[i]);
-        }
-        raise = raise || mx[t] > m[t] + 8.f;
-      }
-      if (__ballot(raise) != 0) {
-        const float change = rmax > R ? kv_raise_unit(rmax, R, invR) : 1.f;
+      // V's scales in units of R: they go into the exponent.  R is raised
+      // (and what is in its units brought along) when one passes it.
+      f32x4 unit = sv * invR;
+      if (__builtin_amdgcn_readfirstlane(kv_max3(__builtin_fmaxf(unit[0], unit[1]), unit[2], unit[3]) > 1.f)) {
+        const float change = kv_raise_unit(kv_max3(__builtin_fmaxf(sv[0], sv[1]), sv[2], sv[3]), R, invR);
+        unit = sv * invR;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          const float mn = __builtin_fmaxf(m[t], kv_col_max(mx[t]));
-          const float alpha = mn == -__builtin_inff() ? 1.f : kv_exp2(m[t] - mn);
-          m[t] = mn;
-          l[t] *= alpha;
+          sums[t][0] *= change;
 #pragma unroll
-          for (int n = 0; n < N; ++n) o[t][n] *= alpha * change;
+          for (int n = 0; n < N; ++n) {
+            kv_stay<D>(o[t][n]);
+            o[t][n] *= change;
+            kv_stay<D>(o[t][n]);
+          }
         }
       }
+      f32x4 log_unit;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) log_unit[i] = __builtin_amdgcn_logf(unit[i]);
       half8_t pb[2][2];
-      // V's scale in units of R goes into the exponent, and a block's sum is
-      // divided by it once.  Scales below 2^-40 R count as that: their
-      // probabilities are 0 in fp16 either way.
-      f32x4 log_unit, per_unit;
-      bool fine = true;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float unit = __builtin_fmaxf(sv[i] * invR, 0x1p-40f);
-        fine = fine && unit >= 0x1p-6f;
-        log_unit[i] = __builtin_amdgcn_logf(unit);
-        per_unit[i] = __builtin_amdgcn_rcpf(unit);
-      }
-      float base[2];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        base[t] = m[t] == -__builtin_inff() ? 0.f : m[t];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            pb[t][i >> 1][(i & 1) * 4 + e] = (_Float16)kv_exp2(__builtin_fmaf(y[t][i][e], c[i], log_unit[i] - base[t]));
-      }
-      if (__builtin_amdgcn_readfirstlane(fine)) {
+      const auto weigh = [&] {
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const half8_t v = pb[t][i >> 1];
-            const half2_t one = {(_Float16)1.f, (_Float16)1.f};
-            const half2_t a = i & 1 ? half2_t{v[4], v[5]} : half2_t{v[0], v[1]}, b = i & 1 ? half2_t{v[6], v[7]} : half2_t{v[2], v[3]};
-            const float sum = __builtin_amdgcn_fdot2(a, one, __builtin_amdgcn_fdot2(b, one, 0.f, false), false);
-            l[t] = __builtin_fmaf(sum, per_unit[i], l[t]);
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              pb[t][i >> 1][(i & 1) * 4 + e] = (_Float16)kv_exp2(__builtin_fmaf(y[t][i][e], c[i], log_unit[i] - base[t]));
+      };
+      // The maximum stays as it is unless a probability passes 2^8: found on
+      // the packed ones, which are half as many as the scores.
+      bool raise = fresh;
+      if (!fresh) {
+        weigh();
+        uint32_t top = 0;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const u32x4_t w = __builtin_bit_cast(u32x4_t, pb[t][h]);
+            top = kv_pk_max3(kv_pk_max3(top, w[0], w[1]), w[2], w[3]);
           }
+        raise = __ballot(top > 0x5C00FFFFu || (top & 0xFFFFu) > 0x5C00u) != 0;
+      }
+      if (raise) {
+        fresh = false;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          float mx = -__builtin_inff();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float most = kv_max3(kv_max3(y[t][i][0], y[t][i][1], y[t][i][2]), y[t][i][3], y[t][i][3]);
+            mx = __builtin_fmaxf(mx, most * c[i]);
+          }
+          const float mn = __builtin_fmaxf(m[t], kv_col_max(mx));
+          const float alpha = mn == -__builtin_inff() ? 1.f : kv_exp2(m[t] - mn);
+          m[t] = mn;
+          base[t] = mn == -__builtin_inff() ? 0.f : mn;
+          fresh = fresh || __ballot(mn == -__builtin_inff()) != 0;
+          l[t] *= alpha;
+          sums[t] *= alpha;
+#pragma unroll
+          for (int n = 0; n < N; ++n) {
+            kv_stay<D>(o[t][n]);
+            o[t][n] *= alpha;
+            kv_stay<D>(o[t][n]);
+          }
+        }
+        weigh();
+      }
+      // what the sums' operand holds for the tokens of block i
+      u32x4_t per;
+      if (__builtin_amdgcn_readfirstlane(kv_min4(unit) >= 0x1p-6f)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float back = __builtin_amdgcn_rcpf(unit[i]);
+          const float hi = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, back) & 0xFFFFE000u);
+          const float v = __builtin_fmaf(back, pick_all, __builtin_fmaf(hi, pick_hi, pick_off));
+          per[i] = __builtin_bit_cast(uint32_t, half2_t{(_Float16)v, (_Float16)v});
+        }
       } else {
         // a block of V far below the others: its rounded probabilities say
         // too little of their sum
@@ -260,6 +329,14 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
           for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) l[t] += kv_exp2(__builtin_fmaf(y[t][i][e], c[i], -base[t]));
+        const uint32_t off = __builtin_bit_cast(uint32_t, half2_t{(_Float16)pick_off, (_Float16)pick_off});
+        per = u32x4_t{off, off, off, off};
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const half8_t a = __builtin_bit_cast(half8_t, u32x4_t{per[2 * h], per[2 * h], per[2 * h + 1], per[2 * h + 1]});
+        sums[0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pb[0][h], sums[0], 0, 0, 0);
+        sums[1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pb[1][h], sums[1], 0, 0, 0);
       }
 #pragma unroll
       for (int n = 0; n < N; ++n)
@@ -269,7 +346,7 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
           o[0][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pb[0][h], o[0][n], 0, 0, 0);
           o[1][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pb[1][h], o[1][n], 0, 0, 0);
         }
-      kv_order_reads<2 * N>();
+      kv_order_reads<2 * N, 4>();
     }
     stage(buf ^ 1, next < 0 ? 0 : s.len - j0 - kKvPage);
     here = next;
@@ -280,22 +357,24 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
   float* mine = p.part + ((int64_t)(w.slot + w.split) * p.kv_heads + head) * SLOT;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    const float sum = kv_col_sum(l[t]);
+    const float sum = kv_col_sum(l[t]) + (sums[t][1] + sums[t][2]);
+    const float unit = R * kKvUnit<BYTES>;  // of o
     const int in = 32 * wave + 16 * t + r, row = row0 + in;
     if (row >= rows) continue;
     if (w.parts == 1) {
       const int token = row / p.group, qh = head * p.group + row - token * p.group;
-      const float inv = sum > 0.f ? R / sum : 0.f;  // nothing seen: zeros
+      const float inv = sum > 0.f ? unit / sum : 0.f;  // nothing seen: zeros
       _Float16* dst = p.out + (int64_t)(s.q0 + token) * p.out_stride + qh * D + 4 * g;
 #pragma unroll
       for (int n = 0; n < N; ++n) {
-        const f32x4 v = o[t][n] * inv;
+        const f32x4 v = (o[t][n] - sums[t][0]) * inv;
         *reinterpret_cast<half4_t*>(dst + 16 * n) = half4_t{(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
       }
     } else {
       if (g == 0) *reinterpret_cast<float2*>(mine + 2 * in) = make_float2(m[t], sum);
 #pragma unroll
-      for (int n = 0; n < N; ++n) *reinterpret_cast<f32x4*>(mine + 2 * kPromptRows + in * D + 16 * n + 4 * g) = o[t][n] * R;
+      for (int n = 0; n < N; ++n) *reinterpret_cast<f32x4*>(mine + 2 * kPromptRows + in * D + 16 * n + 4 * g) =
+            (o[t][n] - sums[t][0]) * unit;
     }
   }
 }
