@@ -86,8 +86,10 @@ constexpr int kRopeTable = 2048;
 // A workgroup's `tokens` rows from `token0`: the angles of its tokens go to
 // LDS once for all heads, then a thread turns units, four at a time with
 // their loads in flight together.  Bound by HBM; the table costs one pair a
-// thread for every token of 128 dimensions.  Every unit is read whole before
-// it is written, so y may be x.
+// thread for every token of 128 dimensions (angles formed by each unit
+// instead: 85 us for 35 us).  Every unit is read whole before it is written,
+// so y may be x.  Measured: 8191 tokens of 48 heads of 128, three axes, 35 us
+// (5.8 TB/s read and written), 5 tokens 3.5 us.
 __device__ __forceinline__ void rope_rows(const RopeRows& p, const RopeAngles& a, int token0, int tokens, int thread,
                                           int threads, float2* table) {
   const int half = a.rot >> 1;
@@ -176,8 +178,11 @@ __device__ __forceinline__ void kv_transpose4(const uint32_t (&x)[4], uint32_t (
 // PER of the page's four blocks, the first D of them K and the others V; a
 // thread holds one unit of one token of each: all loads first, then the
 // largest values of the blocks (one exchange through LDS), then the codes,
-// which go through LDS to be written in page order.  The angles of a unit are formed by the thread
-// that turns it, from frequencies and positions in LDS.
+// which go through LDS to be written in page order.  The angles of a unit are
+// formed by the thread that turns it, from frequencies and positions in LDS.
+// Long calls are bound by HBM, short ones by the chain of latencies from the
+// table to the page.  Measured, 8 heads of 128 and q of 48: 4093 tokens 31 us
+// (4.5 TB/s), one token each of 32 sequences 7.7 us.
 template <int PER>
 __global__ __launch_bounds__(PER == 4 ? 512 : 1024) void kv_append_kernel(KvAppendParams p) {
   __shared__ float red[2][kKvBlocks][4];
@@ -372,7 +377,8 @@ __device__ __forceinline__ void kv_put16(int format, const uint4& c, float scale
 // One workgroup per (page, head) that the last tokens of a sequence lie in.
 // K's 16-byte units are 16 dimensions of a token and go straight to their
 // row; V's are four tokens of each block, turned into rows through LDS.
-// Tokens that no page holds are written as zeros.
+// Tokens that no page holds are written as zeros.  Bound by HBM once it fills
+// the chip.  Measured: 4096 tokens of 8 heads of 128 8.4 us (3 TB/s).
 __global__ __launch_bounds__(256) void kv_read_kernel(KvReadParams p) {
   __shared__ __align__(16) uint8_t rows[kKvPage * 256];
   const int D = p.head_dim, units = D >> 4;

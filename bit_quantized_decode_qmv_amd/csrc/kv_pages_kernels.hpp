@@ -11,6 +11,9 @@
 // The whole-chip kernel is bound by HBM (a page is layers * kv_heads *
 // (128 D + 32) bytes, read and written); the plan by the latency of its few
 // dependent rounds, which is why it only scans refs as far as it needs.
+// Measured with 600 pages of 2 MB: plan of a fork into 8 rows 5.2 us and 7.0
+// us to carry it out, of a resize 6.6 and 5.0, of a compaction 4.7 and, with
+// 143 moves, 123 us (4.9 TB/s).
 #pragma once
 
 #include "kv_common.hpp"

@@ -327,7 +327,8 @@ int bq_spec_decode_verify_noalloc(const void* logits, int logits_dtype, const in
  *   K  [i: 4][c: head_dim/64][g: 4][t: 16][j: 16]  token 16i + t, dim 64c + 16g + j
  *   V  [n: head_dim/16][g: 4][d: 16][i: 4][j: 4]   token 16i + 4g + j, dim 16n + d
  * head_dim 64, 128, 192 or 256; kv_heads 1..1024; layers 1..4096; scales are
- * not negative; codes and scales 16-byte aligned.  layer selects one layer of the arrays; page calls work on all.
+ * not negative; codes and scales 16-byte aligned.  layer selects one layer of
+ * the arrays; page calls work on all.
  *
  * The batch of a call.  Sequence b has the rows cu[b] .. cu[b+1] - 1 of the
  * call's packed row arrays (cu: int32 [batch + 1], rising, cu[batch] =
@@ -404,8 +405,12 @@ int bq_kv_read(const bq_kv_cache* cache, int layer, void* k, void* v, const int*
  * sees, with the key/value head h / (q_heads / kv_heads).  With BQ_KV_CAUSAL
  * a row at position n sees j <= n, and with window > 0 only j > n - window;
  * without it every row sees all lens[b] tokens (an encoder's states).  A row
- * that sees nothing gives zeros.  Scores, sums and outputs in fp32, codes
- * exact, probabilities rounded to fp16 for the product with V.
+ * that sees nothing gives zeros; tokens that no page holds are not seen.
+ * Scores, sums and outputs in fp32, codes exact.  Up to 16 rows of a
+ * key/value head and sequence on average (rows times q_heads / kv_heads; 32
+ * where head_dim <= 128) the probabilities enter the product with V as sums
+ * of two fp16 numbers; beyond that they are rounded to fp16 once and divided
+ * by the sum of the rounded ones.
  *
  * workspace (device memory, 16-byte aligned, or NULL): lets the tokens of a
  * long sequence be shared by several workgroups.  Its first
@@ -413,7 +418,9 @@ int bq_kv_read(const bq_kv_cache* cache, int layer, void* k, void* v, const int*
  * leaves them zero again.  bq_kv_attn_workspace gives the size of the full
  * split; less gives a smaller split or none, with results that may differ
  * in the last bits.  Calls that overlap in time must not share a workspace.
- * One launch; the same bits on every call with the same arguments. */
+ * The same bits on every call with the same arguments; one launch, two where
+ * many rows are split (more past 32768 tiles of a head).  Rows of a call
+ * whose cu falls somewhere may be left unwritten. */
 #define BQ_KV_CAUSAL 1
 #define BQ_KV_ATTN_COUNTER_BYTES 65536
 int bq_kv_attn_workspace(const bq_kv_cache* cache, int q_heads, int batch, int total, size_t* bytes);
