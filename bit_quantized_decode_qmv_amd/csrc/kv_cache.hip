@@ -21,9 +21,16 @@ RopeAngles angles(const int* pos, const float* inv_freq, const int* axis, int ro
   return RopeAngles{pos, inv_freq, axis, rot_dim, axes, (flags & BQ_ROPE_ADJACENT) ? 1 : 0, total};
 }
 // Tokens a workgroup rotates: one while the tokens are few, more once they
-// fill the chip several times over, as far as the table of angles holds them.
-int rope_tokens_per_wg(int tokens, int rot_dim) {
-  return std::clamp(tokens / 512, 1, std::min(8, 2 * kRopeTable / std::max(rot_dim, 1)));
+// fill the chip several times over, as far as the table of angles holds them;
+// of these numbers the one whose units best fill the rounds of its threads.
+int rope_tokens_per_wg(int tokens, int rot_dim, int units, int threads) {
+  const int most = std::clamp(tokens / 512, 1, std::min(8, 2 * kRopeTable / std::max(rot_dim, 1)));
+  const int64_t round = (int64_t)kRopeAtOnce * threads;
+  const auto fill = [&](int t) { return (double)t * units / (double)(((int64_t)t * units + round - 1) / round); };
+  int best = 1;
+  for (int t = 2; t <= most; ++t)
+    if (fill(t) >= fill(best)) best = t;
+  return best;
 }
 
 }  // namespace
@@ -43,7 +50,7 @@ int bq_rope(const void* x, void* y, long long x_stride, long long y_stride, int 
   RopeParams p{};
   p.rows = RopeRows{static_cast<const _Float16*>(x), static_cast<_Float16*>(y), x_stride, y_stride, heads, head_dim};
   p.a = angles(pos, inv_freq, axis, rot_dim, axes, flags, tokens);
-  p.tokens_per_wg = rope_tokens_per_wg(tokens, rot_dim);
+  p.tokens_per_wg = rope_tokens_per_wg(tokens, rot_dim, heads * head_dim / 16, 256);
   return kv_launch(reinterpret_cast<const void*>(&rope_kernel),
                    dim3((unsigned)((tokens + p.tokens_per_wg - 1) / p.tokens_per_wg)), dim3(256), 0, stream, &p);
 }
@@ -84,19 +91,20 @@ int bq_kv_append(const bq_kv_cache* cache, int layer, const void* k, const void*
   p.format = cache->format;
   // n tokens lie in at most (n + 126) / 64 pages
   const int64_t items = ((int64_t)total + (int64_t)std::min(batch, total) * 126) / kKvPage * cache->kv_heads;
-  p.q_tokens_per_wg = rope_tokens_per_wg(total, rot_dim);
-  const int64_t q_wgs = q ? (total + p.q_tokens_per_wg - 1) / p.q_tokens_per_wg : 0;
-  if (items + q_wgs > 0x7FFFFFFF) return BQ_ERR_SHAPE;
-  p.items = (int)items;
   // Blocks of a page a thread: one (two where heads are wide) while the pages
   // are fewer than the CUs and written whole, else all four.  Measured, 8
   // heads of 128: 128 tokens 13.1 us with one and 16.8 with four, 4093 tokens
   // 50 and 38.7.
   const int per = total < 16 * (int64_t)batch || items > 256 ? 4 : D <= 128 ? 1 : 2;
+  const int threads = 2 * D * (kKvBlocks / per);
+  p.q_tokens_per_wg = rope_tokens_per_wg(total, rot_dim, q_heads * D / 16, threads);
+  const int64_t q_wgs = q ? (total + p.q_tokens_per_wg - 1) / p.q_tokens_per_wg : 0;
+  if (items + q_wgs > 0x7FFFFFFF) return BQ_ERR_SHAPE;
+  p.items = (int)items;
   const void* fn = per == 4 ? reinterpret_cast<const void*>(&kv_append_kernel<4>)
                  : per == 2 ? reinterpret_cast<const void*>(&kv_append_kernel<2>)
                             : reinterpret_cast<const void*>(&kv_append_kernel<1>);
-  return kv_launch(fn, dim3((unsigned)(items + q_wgs)), dim3((unsigned)(2 * D * (kKvBlocks / per))), 0, stream, &p);
+  return kv_launch(fn, dim3((unsigned)(items + q_wgs)), dim3((unsigned)threads), 0, stream, &p);
 }
 
 int bq_kv_read(const bq_kv_cache* cache, int layer, void* k, void* v, const int* cu, const int* lens, const int* table,

@@ -82,6 +82,7 @@ struct RopeRows {
 
 // (cos, sin) of the tokens at hand, formed once for all heads.
 constexpr int kRopeTable = 2048;
+constexpr int kRopeAtOnce = 4;  // units of a thread whose loads are in flight together
 
 // A workgroup's `tokens` rows from `token0`: the angles of its tokens go to
 // LDS once for all heads, then a thread turns units, four at a time with
@@ -99,7 +100,7 @@ __device__ __forceinline__ void rope_rows(const RopeRows& p, const RopeAngles& a
   }
   __syncthreads();
   const int units = p.head_dim >> 4, per = p.heads * units, all = tokens * per;
-  constexpr int AT_ONCE = 4;
+  constexpr int AT_ONCE = kRopeAtOnce;
   for (int i0 = thread; i0 < all; i0 += AT_ONCE * threads) {
     half8_t v[AT_ONCE][2];
     int lo[AT_ONCE], hi[AT_ONCE], tok[AT_ONCE], unit[AT_ONCE], at[AT_ONCE];
