@@ -92,10 +92,11 @@ int bq_kv_append(const bq_kv_cache* cache, int layer, const void* k, const void*
   // n tokens lie in at most (n + 126) / 64 pages
   const int64_t items = ((int64_t)total + (int64_t)std::min(batch, total) * 126) / kKvPage * cache->kv_heads;
   // Blocks of a page a thread: one (two where heads are wide) while the pages
-  // are fewer than the CUs and written whole, else all four.  Measured, 8
-  // heads of 128: 128 tokens 13.1 us with one and 16.8 with four, 4093 tokens
-  // 50 and 38.7.
-  const int per = total < 16 * (int64_t)batch || items > 256 ? 4 : D <= 128 ? 1 : 2;
+  // are fewer than half the CUs and written whole, else all four.  Measured, 8
+  // heads of 128: 128 tokens 13.1 us with one and 16.8 with four, 1500 tokens
+  // 26.0 and 23.4, 4093 tokens 50 and 38.7; 4 heads of 256: 300 tokens 17.7 us
+  // with two and 20.6 with four, eight times 301 tokens 31.6 and 27.0.
+  const int per = total < 16 * (int64_t)batch || items > 128 ? 4 : D <= 128 ? 1 : 2;
   const int threads = 2 * D * (kKvBlocks / per);
   p.q_tokens_per_wg = rope_tokens_per_wg(total, rot_dim, q_heads * D / 16, threads);
   const int64_t q_wgs = q ? (total + p.q_tokens_per_wg - 1) / p.q_tokens_per_wg : 0;

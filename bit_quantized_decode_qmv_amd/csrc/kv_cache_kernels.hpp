@@ -407,6 +407,18 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvReadParams p) {
   const u32x4_t* v = reinterpret_cast<const u32x4_t*>(p.v + head_at * kKvPage * D);
   const int t0 = max(s.len - s.n - at * kKvPage, 0), t1 = min(s.len - at * kKvPage, kKvPage);
   const int64_t row0 = s.q0 + at * kKvPage - (s.len - s.n);  // row of the page's token t: row0 + t
+  // K's units and the scales are requested ahead of V, D / 64 a thread
+  const int all = (t1 - t0) * units;  // at least one: the page holds some of the rows
+  uint4 kc[4];
+  float ks[4], vs[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (j * 64 >= D) continue;
+    const int i = min((int)threadIdx.x + j * 256, all - 1), t = t0 + i / units;
+    kc[j] = k[kv_k_at(t, i % units * 16, D) >> 4];
+    ks[j] = p.ks[head_at * kKvBlocks + t / kKvBlock];
+    vs[j] = p.vs[head_at * kKvBlocks + t / kKvBlock];
+  }
   for (int i = (int)threadIdx.x; i < D; i += 256) {
     // four dimensions (dim ..) of the tokens 16i + 4g ..
     const int g = i / (D >> 2), dim = (i - g * (D >> 2)) * 4;
@@ -423,14 +435,20 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvReadParams p) {
     }
   }
   __syncthreads();
-  const uint4 zero = p.format == BQ_KV_I8 ? make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u) : make_uint4(0, 0, 0, 0);
-  for (int i = (int)threadIdx.x; i < (t1 - t0) * units; i += 256) {
+  const uint32_t zero = p.format == BQ_KV_I8 ? 0x80808080u : 0u;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int i = (int)threadIdx.x + j * 256;
+    if (i >= all) break;
     const int t = t0 + i / units, u = i % units;
     const int64_t to = ((row0 + t) * p.kv_heads + head) * D + u * 16;
-    const int64_t sc = head_at * kKvBlocks + t / kKvBlock;
-    kv_put16(p.format, page < 0 ? zero : k[kv_k_at(t, u * 16, D) >> 4], page < 0 ? 0.f : p.ks[sc], p.ok + to);
-    kv_put16(p.format, page < 0 ? zero : *reinterpret_cast<const uint4*>(&rows[t * D + u * 16]), page < 0 ? 0.f : p.vs[sc],
-             p.ov + to);
+    uint4 vc = *reinterpret_cast<const uint4*>(&rows[t * D + u * 16]);
+    if (page < 0) {
+      kc[j] = vc = make_uint4(zero, zero, zero, zero);
+      ks[j] = vs[j] = 0.f;
+    }
+    kv_put16(p.format, kc[j], ks[j], p.ok + to);
+    kv_put16(p.format, vc, vs[j], p.ov + to);
   }
 }
 
