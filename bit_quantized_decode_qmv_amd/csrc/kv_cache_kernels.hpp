@@ -182,8 +182,8 @@ __device__ __forceinline__ void kv_transpose4(const uint32_t (&x)[4], uint32_t (
 // which go through LDS to be written in page order.  The angles of a unit are
 // formed by the thread that turns it, from frequencies and positions in LDS.
 // Long calls are bound by HBM, short ones by the chain of latencies from the
-// table to the page.  Measured, 8 heads of 128 and q of 48: 4093 tokens 31 us
-// (4.5 TB/s), one token each of 32 sequences 7.7 us.
+// table to the page.  Measured, 8 heads of 128 and q of 48: 4093 tokens 30 us
+// (4.2 TB/s), one token each of 32 sequences 7.7 us.
 template <int PER>
 __global__ __launch_bounds__(PER == 4 ? 512 : 1024) void kv_append_kernel(KvAppendParams p) {
   __shared__ float red[2][kKvBlocks][4];
