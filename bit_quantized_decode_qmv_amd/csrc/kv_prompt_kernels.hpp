@@ -269,10 +269,13 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
             for (int e = 0; e < 4; ++e)
               pb[t][i >> 1][(i & 1) * 4 + e] = (_Float16)kv_exp2(__builtin_fmaf(y[t][i][e], c[i], log_unit[i] - base[t]));
       };
-      // The maximum stays as it is unless a probability passes 2^8: found on
-      // the packed ones, which are half as many as the scores.
-      bool raise = fresh;
-      if (!fresh) {
+      // The maximum stays as it is unless a probability, in V's units, passes
+      // 2^8: found on the packed ones, which are half as many as the scores.
+      // A block of V far below the others (fine false) would hide how large
+      // the probability itself is: there the scores are looked at.
+      const bool fine = __builtin_amdgcn_readfirstlane(kv_min4(unit) >= 0x1p-6f);
+      bool raise = fresh || !fine;
+      if (!raise) {
         weigh();
         uint32_t top = 0;
 #pragma unroll
@@ -312,7 +315,7 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
       }
       // what the sums' operand holds for the tokens of block i
       u32x4_t per;
-      if (__builtin_amdgcn_readfirstlane(kv_min4(unit) >= 0x1p-6f)) {
+      if (fine) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float back = __builtin_amdgcn_rcpf(unit[i]);
@@ -321,8 +324,7 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
           per[i] = __builtin_bit_cast(uint32_t, half2_t{(_Float16)v, (_Float16)v});
         }
       } else {
-        // a block of V far below the others: its rounded probabilities say
-        // too little of their sum
+        // the rounded probabilities of such a block say too little of their sum
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll

@@ -73,6 +73,33 @@ def test_windows_in_parts(window, new):
     run(np.random.default_rng(36), "int8", 64, 1, 2, [6000, 90], [new, new], window=window)
 
 
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("new", [1, 5, 60])
+def test_scores_that_leap_over_blocks_without_values(fmt, new):
+    """A page whose V is zero (scale 0) has scores 200 above the page before, and the page after it 300 more: sums that
+    followed V's units only would pass the range of fp32.  A page's keys are equal, so its scores are."""
+    import bit_quantized_decode_qmv_amd as bq
+    rng = np.random.default_rng(43)
+    D, lens = 64, [256, 200]
+    table, pages = synth.make_kv_table(rng, lens)
+    c = synth.make_kv_pool(rng, 1, pages, 1, D, fmt)
+    c["k"][:] = 128 + 127 if fmt == "int8" else 0x7E          # the largest code
+    for row in table:
+        for at, score in enumerate((0, 200, 500, 0)):
+            if row[at] >= 0:
+                # q = 1 in every dimension, scale 1/8: 8 scale code = score
+                c["ks"][0, row[at]] = score / 8 / (127 if fmt == "int8" else 448)
+                if at == 1:
+                    c["vs"][0, row[at]] = 0
+    q = np.ones((2 * new, 2, D), np.float16)
+    cu = cu_of([new] * 2)
+    for causal in (True, False):
+        for workspace in (None, torch_mod().zeros(0, dtype=torch_mod().uint8, device="cuda:0")):
+            out = bq.kv_attn(upload_cache(c), 0, up(q), up(cu), up(lens, np.int32), up(table), causal=causal,
+                             workspace=workspace)
+            check(out.cpu().numpy(), c, 0, table, lens, cu, q, 0.125, causal, 0)
+
+
 def test_same_bits_on_every_call():
     import bit_quantized_decode_qmv_amd as bq
     torch = torch_mod()
