@@ -140,7 +140,7 @@ int bq_kv_attn(const bq_kv_cache* cache, int layer, const void* q, void* out, lo
   p.kv_heads = cache->kv_heads;
   p.group = q_heads / cache->kv_heads;
   p.causal = flags & BQ_KV_CAUSAL;
-  p.window = window;
+  p.window = std::min(window, 1 << 30);  // no sequence is longer; a row's place may be negative
   p.scale = scale * 1.44269504f;
   const Plan pl = plan(cache, q_heads, batch, total, max_pages, workspace ? workspace_bytes : 0);
   p.target = (int)pl.target;

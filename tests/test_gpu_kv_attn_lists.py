@@ -100,6 +100,14 @@ def test_scores_that_leap_over_blocks_without_values(fmt, new):
             check(out.cpu().numpy(), c, 0, table, lens, cu, q, 0.125, causal, 0)
 
 
+@pytest.mark.parametrize("news", [[3, 2], [60, 40]])
+def test_windows_longer_than_any_sequence(news):
+    """The largest window is no window, also where rows are more than tokens."""
+    lens = [20, 70]
+    out = [run(np.random.default_rng(44), "int8", 64, 1, 2, lens, news, window=w)[0] for w in (0, 1 << 30, 2 ** 31 - 1)]
+    assert np.array_equal(out[0], out[1]) and np.array_equal(out[0], out[2])
+
+
 def test_same_bits_on_every_call():
     import bit_quantized_decode_qmv_amd as bq
     torch = torch_mod()
