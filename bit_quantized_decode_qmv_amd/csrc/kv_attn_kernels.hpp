@@ -130,7 +130,13 @@ __device__ __forceinline__ bool kv_attn_work(const KvAttnParams& p, int item, Kv
     // 32 pages 14.4 us in parts of 16 and 11.9 in parts of 8; 2047 pages of
     // one head 28.6 us in parts of 16 and 41.1 in parts of 8)
     const int least = p.min_pages > 0 ? p.min_pages : all <= 16 || all > 64 ? 16 : 8;
-    w.chunk = max((int)(((unsigned)all + p.target - 1) / (unsigned)p.target), least);
+    // A quarter more than an even share, few rows: every tile's last part comes
+    // on top of the whole ones, and would run in a second round.  Measured, 8
+    // heads of 128, even shares and a quarter more: 4 sequences of up to 30000
+    // tokens 31.4 us and 24.4, 16 of up to 16000 47.9 and 41.2, 64 of up to
+    // 4100 44.6 and 41.7; five rows each of 32 of up to 16384 87.9 and 89.2.
+    const unsigned share = ROWS <= 32 ? (unsigned)all + (unsigned)all / 4 : (unsigned)all;
+    w.chunk = max((int)((share + p.target - 1) / (unsigned)p.target), least);
   }
   // whole parts ahead of a tile's last one
   const auto whole = [&](const KvSeq& s) { return (int)((unsigned)(pages(s) - 1) / (unsigned)w.chunk); };
@@ -273,7 +279,7 @@ constexpr int kv_waves(int D) { return D <= 128 ? 8 : 4; }
 // Measured, 8 heads of 128 with 6 query heads each: one row over 131001
 // tokens 55 us (4.9 TB/s of codes), over 1003 tokens 9.6 us (a launch, the
 // table, one page a wave and the join); five rows each of 32 sequences of
-// 1024 to 16384 tokens (e4m3) 82 us (4.6 TB/s).
+// 1024 to 16384 tokens (e4m3) 87 us (4.3 TB/s).
 template <int D, int FMT, int RT>
 __global__ __launch_bounds__(64 * kv_waves(D)) void kv_attn_rows_kernel(KvAttnParams p) {
   constexpr int C = D / 64, N = D / 16, ROWS = 16 * RT, NW = kv_waves(D), THREADS = 64 * NW;
