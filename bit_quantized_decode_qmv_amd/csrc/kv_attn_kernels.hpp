@@ -355,7 +355,7 @@ __global__ __launch_bounds__(64 * kv_waves(D)) void kv_attn_rows_kernel(KvAttnPa
   for (int t = 0; t < RT; ++t) q_off[t] = kv_query_offset<BYTES>(q[t]);
   const half8_t ones = kv_offset_operand<BYTES>();
 
-  f32x4 o[RT][N], o_off[RT];  // o_off: what the codes' offset adds to each o
+  f32x4 o[RT][N], o_off[RT];  // o_off: what the codes' offset has added to each o since it was last taken off
   float m[RT], l[RT];
   float R = 0x1p-100f, invR = 0x1p100f;  // o is in units of R, a power of two near the largest scale of V so far
 #pragma unroll
@@ -450,6 +450,14 @@ __global__ __launch_bounds__(64 * kv_waves(D)) void kv_attn_rows_kernel(KvAttnPa
         o_off[t] *= alpha * change;
 #pragma unroll
         for (int n = 0; n < N; ++n) o[t][n] *= alpha * change;
+      }
+    }
+    if (BYTES && k % kKvOffsetRowPages == 0) {
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) o[t][n] -= o_off[t];
+        o_off[t] = f32x4{0.f, 0.f, 0.f, 0.f};
       }
     }
     half8_t ph_[RT][2], pl_[RT][2];

@@ -164,8 +164,9 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
 
   f32x4 o[2][N];
   // Sums over the rounded probabilities, by the matrix cores: rows 4g + e of
-  // one more operand hold, e = 0, V's code offset and, 1 and 2, the two fp16
-  // terms of what takes V's scale out again.
+  // one more operand hold, e = 0, V's code offset (taken off o whenever the
+  // maximum is looked at, kKvOffsetPages pages later at most) and, 1 and 2, the
+  // two fp16 terms of what takes V's scale out again.
   f32x4 sums[2];
   const int term = lane & 3;
   const float pick_all = term == 2 ? 1.f : 0.f, pick_hi = term == 1 ? 1.f : term == 2 ? -1.f : 0.f;
@@ -274,7 +275,7 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
       // A block of V far below the others (fine false) would hide how large
       // the probability itself is: there the scores are looked at.
       const bool fine = __builtin_amdgcn_readfirstlane(kv_min4(unit) >= 0x1p-6f);
-      bool raise = fresh || !fine;
+      bool raise = fresh || !fine || (BYTES && at % kKvOffsetPages == 0);
       if (!raise) {
         weigh();
         uint32_t top = 0;
@@ -303,13 +304,13 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
           base[t] = mn == -__builtin_inff() ? 0.f : mn;
           fresh = fresh || __ballot(mn == -__builtin_inff()) != 0;
           l[t] *= alpha;
-          sums[t] *= alpha;
 #pragma unroll
           for (int n = 0; n < N; ++n) {
             kv_stay<D>(o[t][n]);
-            o[t][n] *= alpha;
+            o[t][n] = BYTES ? (o[t][n] - sums[t][0]) * alpha : o[t][n] * alpha;
             kv_stay<D>(o[t][n]);
           }
+          sums[t] = f32x4{0.f, sums[t][1] * alpha, sums[t][2] * alpha, 0.f};
         }
         weigh();
       }
