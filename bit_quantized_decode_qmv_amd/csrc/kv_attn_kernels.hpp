@@ -35,6 +35,14 @@ struct KvAttnParams {
 
 constexpr int kKvMaxParts = 128;  // of a tile
 
+// Probabilities enter the second product as fp16 numbers.  They are formed as
+// 2^(score - maximum + kKvLift) and, between two looks at the maximum, grow to
+// 2^15: all of fp16's range lies below them, so a term's steps end at 2^-31 of
+// the largest one (V's scale included) and not at 2^-24.  Where one token has
+// most of the weight and no value, the result is the sum of terms near 2^-20.
+// Sums carry the same factor, so it leaves with the division.
+constexpr float kKvLift = 7.f;
+
 __device__ __forceinline__ float kv_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // max / sum over the four lanes of a column (lanes l, l ^ 16, l ^ 32, l ^ 48)
@@ -272,9 +280,10 @@ constexpr int kv_waves(int D) { return D <= 128 ? 8 : 4; }
 // The running maximum is raised only when a score passes it by more than 8
 // (in log2): then the four lanes of a column agree on a new one and the
 // outputs are rescaled.  Otherwise a page costs no step across lanes, and the
-// probabilities, at most 2^8, stay well inside fp16.  They are taken as the
-// sum of two fp16 numbers, so that no more than 2^-22 of a probability is
-// lost: the second product is cheap beside the loads.
+// probabilities, at most 2^15 (kKvLift), stay inside fp16.  They are taken as
+// the sum of two fp16 numbers: what is lost of a term is no more than 2^-22 of
+// it, or 2^-32 of the largest possible one.  The second product is cheap
+// beside the loads.
 //
 // Measured, 8 heads of 128 with 6 query heads each: one row over 131001
 // tokens 55 us (4.9 TB/s of codes), over 1003 tokens 9.6 us (a launch, the
@@ -465,7 +474,7 @@ __global__ __launch_bounds__(64 * kv_waves(D)) void kv_attn_rows_kernel(KvAttnPa
     load_scales(next);
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-      const float base = m[t] == -__builtin_inff() ? 0.f : m[t];  // a row that has seen nothing yet
+      const float base = m[t] == -__builtin_inff() ? 0.f : m[t] - kKvLift;  // (0: a row that has seen nothing yet)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll

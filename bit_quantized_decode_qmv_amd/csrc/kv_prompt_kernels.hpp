@@ -11,9 +11,10 @@
 // products while the other is in its softmax.
 //
 // The probabilities are rounded to fp16 (nearest even) once, with V's block
-// scale folded in: 2^-12 of each on average, as the rounding of the result.
-// Their sum is taken of the rounded ones, so that a row that sees few tokens
-// does not keep the rounding of a common factor.
+// scale folded in: by up to 2^-11 of each, 2^-12 on average, as the rounding of
+// the result, or by 2^-32 of the largest possible one (kKvLift).  Their sum is
+// taken of the rounded ones, so that a row that sees few tokens does not keep
+// the rounding of a common factor.
 //
 // Bound by issue: a wave's page of 128 dimensions is 68 matrix instructions
 // (1090 cycles), some 210 vector instructions (1290, a quarter of them for
@@ -171,7 +172,7 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
   const int term = lane & 3;
   const float pick_all = term == 2 ? 1.f : 0.f, pick_hi = term == 1 ? 1.f : term == 2 ? -1.f : 0.f;
   const float pick_off = term == 0 ? kKvOffset<BYTES> : 0.f;
-  float m[2], l[2], base[2];  // base: the maximum that is taken off, 0 while there is none
+  float m[2], l[2], base[2];  // base: what is taken off a score, the maximum less kKvLift, 0 while there is none
   bool fresh = true;          // some row has seen nothing yet
   float R = 0x1p-100f, invR = 0x1p100f;
 #pragma unroll
@@ -271,7 +272,8 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
               pb[t][i >> 1][(i & 1) * 4 + e] = (_Float16)kv_exp2(__builtin_fmaf(y[t][i][e], c[i], log_unit[i] - base[t]));
       };
       // The maximum stays as it is unless a probability, in V's units, passes
-      // 2^8: found on the packed ones, which are half as many as the scores.
+      // 2^8 (2^15 as it is held): found on the packed ones, which are half as
+      // many as the scores.
       // A block of V far below the others (fine false) would hide how large
       // the probability itself is: there the scores are looked at.
       const bool fine = __builtin_amdgcn_readfirstlane(kv_min4(unit) >= 0x1p-6f);
@@ -286,7 +288,7 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
             const u32x4_t w = __builtin_bit_cast(u32x4_t, pb[t][h]);
             top = kv_pk_max3(kv_pk_max3(top, w[0], w[1]), w[2], w[3]);
           }
-        raise = __ballot(top > 0x5C00FFFFu || (top & 0xFFFFu) > 0x5C00u) != 0;
+        raise = __ballot(top > 0x7800FFFFu || (top & 0xFFFFu) > 0x7800u) != 0;
       }
       if (raise) {
         fresh = false;
@@ -301,7 +303,7 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
           const float mn = __builtin_fmaxf(m[t], kv_col_max(mx));
           const float alpha = mn == -__builtin_inff() ? 1.f : kv_exp2(m[t] - mn);
           m[t] = mn;
-          base[t] = mn == -__builtin_inff() ? 0.f : mn;
+          base[t] = mn == -__builtin_inff() ? 0.f : mn - kKvLift;
           fresh = fresh || __ballot(mn == -__builtin_inff()) != 0;
           l[t] *= alpha;
 #pragma unroll
