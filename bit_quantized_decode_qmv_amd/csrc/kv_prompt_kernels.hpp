@@ -165,9 +165,8 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
 
   f32x4 o[2][N];
   // Sums over the rounded probabilities, by the matrix cores: rows 4g + e of
-  // one more operand hold, e = 0, V's code offset (taken off o whenever the
-  // maximum is looked at, kKvOffsetPages pages later at most) and, 1 and 2, the
-  // two fp16 terms of what takes V's scale out again.
+  // one more operand hold, e = 0, V's code offset (since it was last taken
+  // off o) and, 1 and 2, the two fp16 terms of what takes V's scale out again.
   f32x4 sums[2];
   const int term = lane & 3;
   const float pick_all = term == 2 ? 1.f : 0.f, pick_hi = term == 1 ? 1.f : term == 2 ? -1.f : 0.f;
@@ -277,7 +276,10 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
       // A block of V far below the others (fine false) would hide how large
       // the probability itself is: there the scores are looked at.
       const bool fine = __builtin_amdgcn_readfirstlane(kv_min4(unit) >= 0x1p-6f);
-      bool raise = fresh || !fine || (BYTES && at % kKvOffsetPages == 0);
+      // (Only then does o begin from what may be negative: until then it and
+      // the offset's sum are rounded alike, and a value of 0 comes back as 0.)
+      const bool take_off = BYTES && at % kKvOffsetPages == 0;
+      bool raise = fresh || !fine || take_off;
       if (!raise) {
         weigh();
         uint32_t top = 0;
@@ -306,13 +308,14 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
           base[t] = mn == -__builtin_inff() ? 0.f : mn - kKvLift;
           fresh = fresh || __ballot(mn == -__builtin_inff()) != 0;
           l[t] *= alpha;
+          const float off = take_off ? sums[t][0] : 0.f;
 #pragma unroll
           for (int n = 0; n < N; ++n) {
             kv_stay<D>(o[t][n]);
-            o[t][n] = BYTES ? (o[t][n] - sums[t][0]) * alpha : o[t][n] * alpha;
+            o[t][n] = BYTES ? (o[t][n] - off) * alpha : o[t][n] * alpha;
             kv_stay<D>(o[t][n]);
           }
-          sums[t] = f32x4{0.f, sums[t][1] * alpha, sums[t][2] * alpha, 0.f};
+          sums[t] = f32x4{(sums[t][0] - off) * alpha, sums[t][1] * alpha, sums[t][2] * alpha, 0.f};
         }
         weigh();
       }
