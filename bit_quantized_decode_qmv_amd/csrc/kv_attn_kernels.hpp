@@ -70,14 +70,55 @@ __device__ __forceinline__ uint32_t kv_pk_max3(uint32_t a, uint32_t b, uint32_t 
 __device__ __forceinline__ float kv_min4(f32x4 x) {
   return __builtin_fminf(__builtin_fminf(x[0], x[1]), __builtin_fminf(x[2], x[3]));
 }
-// R becomes the power of two above the scale rmax, invR its reciprocal; what
-// values in units of the old one are multiplied by.
-__device__ __forceinline__ float kv_raise_unit(float rmax, float& R, float& invR) {
-  const uint32_t ex = min(((__builtin_bit_cast(uint32_t, rmax) >> 23) & 255u) + 1, 253u);
-  const float was = R;
-  R = __builtin_bit_cast(float, ex << 23);
-  invR = __builtin_bit_cast(float, (254u - ex) << 23);
-  return was * invR;
+__device__ __forceinline__ float kv_max4(f32x4 x) {
+  return __builtin_fmaxf(__builtin_fmaxf(x[0], x[1]), __builtin_fmaxf(x[2], x[3]));
+}
+
+// The outputs are in units of R, a power of two that follows V's scales from
+// page to page: a term is formed as probability times scale / R, and what is
+// lost of it goes by R.  A page whose scales lie in R's range is taken as it
+// is.  For any other R is fitted to it: above its largest scale, or, where the
+// scales differ by more than 4, above the page's largest term and four times
+// its smallest scale above 0.  So R is at most 64 times that scale, or twice
+// that term, and a block of large values that no row attends to, or sees,
+// takes no bits from the terms beside it, and none from later pages.
+// low, top: the least and the largest of a page's scales / R.
+__device__ __forceinline__ bool kv_in_unit(float low, float top) { return low >= 0x1p-6f && top <= 1.f; }
+// R is held as its exponent, biased by 127.  Below the least one a scale's
+// values are 0 in fp16, whatever their weight.
+constexpr int kKvLeastUnit = 127 - 48;
+__device__ __forceinline__ float kv_exp_float(int ex) { return __builtin_bit_cast(float, (uint32_t)ex << 23); }
+// Fits R to a page whose scales are unit * R and whose largest term is 2^most
+// * R.  Brings unit along; what o is multiplied by.
+template <typename Most>
+__device__ __forceinline__ float kv_fit_unit(f32x4& unit, float low, float top, Most most, int& ex) {
+  if (__builtin_expect(__builtin_amdgcn_readfirstlane(top > 4.f * low), 0)) {
+    low = top;  // of those that are not 0
+#pragma unroll
+    for (int i = 0; i < 4; ++i) low = unit[i] > 0.f ? __builtin_fminf(low, unit[i]) : low;
+    top = __builtin_fminf(top, __builtin_fmaxf(4.f * low, __builtin_amdgcn_exp2f(most())));
+  }
+  const int above = (int)((__builtin_bit_cast(uint32_t, top) >> 23) & 255u) + 1 - 127, was = ex;
+  ex = __builtin_amdgcn_readfirstlane(min(max(ex + above, kKvLeastUnit), 253));
+  const float change = __builtin_ldexpf(1.f, was - ex);
+  unit *= change;
+  return change;
+}
+// max over a wave's lanes, by shifts within rows of 16 and broadcasts across
+// rows (no lane addresses, which would be held all along the page loop)
+template <int STEP, int ROWS>
+__device__ __forceinline__ float kv_max_step(float x) {
+  const int bits = __builtin_bit_cast(int, x);
+  return __builtin_fmaxf(x, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(bits, bits, STEP, ROWS, 0xF, false)));
+}
+__device__ __forceinline__ float kv_wave_max(float x) {
+  x = kv_max_step<0x111, 0xF>(x);  // row_shr:1
+  x = kv_max_step<0x112, 0xF>(x);  // row_shr:2
+  x = kv_max_step<0x114, 0xF>(x);  // row_shr:4
+  x = kv_max_step<0x118, 0xF>(x);  // row_shr:8
+  x = kv_max_step<0x142, 0xA>(x);  // row_bcast:15 into rows 1 and 3
+  x = kv_max_step<0x143, 0xC>(x);  // row_bcast:31 into rows 2 and 3
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 63));
 }
 
 // Values that other workgroups read: stores and loads at device scope, which
@@ -282,7 +323,7 @@ constexpr int kv_waves(int D) { return D <= 128 ? 8 : 4; }
 // outputs are rescaled.  Otherwise a page costs no step across lanes, and the
 // probabilities, at most 2^15 (kKvLift), stay inside fp16.  They are taken as
 // the sum of two fp16 numbers: what is lost of a term is no more than 2^-22 of
-// it, or 2^-32 of the largest possible one.  The second product is cheap
+// it, or 2^-32 of the outputs' unit (kv_in_unit).  The second product is cheap
 // beside the loads.
 //
 // Measured, 8 heads of 128 with 6 query heads each: one row over 131001
@@ -366,7 +407,7 @@ __global__ __launch_bounds__(64 * kv_waves(D)) void kv_attn_rows_kernel(KvAttnPa
 
   f32x4 o[RT][N], o_off[RT];  // o_off: what the codes' offset has added to each o since it was last taken off
   float m[RT], l[RT];
-  float R = 0x1p-100f, invR = 0x1p100f;  // o is in units of R, a power of two near the largest scale of V so far
+  int unit_ex = kKvLeastUnit;  // of R, the unit of o
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
     m[t] = -__builtin_inff();
@@ -421,12 +462,12 @@ __global__ __launch_bounds__(64 * kv_waves(D)) void kv_attn_rows_kernel(KvAttnPa
           for (int e = 0; e < 4; ++e)
             y[t][i][e] = (unsigned)(in + 16 * i + e) < (unsigned)count ? y[t][i][e] : -__builtin_inff();
       }
-      // what lies past the length is never used: neither a scale nor, in
-      // e4m3, a code that is no number
+      // what lies past the length is never used: neither a scale (any in R's
+      // range stands for it) nor, in e4m3, a code that is no number
       if (left < kKvPage) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if (16 * i >= left) sv[i] = 0.f;
+          if (16 * i >= left) sv[i] = left > 0 ? sv[0] : kv_exp_float(unit_ex);
           if constexpr (FMT == BQ_KV_E4M3) {
             const int keep = min(max(left - 16 * i - 4 * g, 0), 4);
             const uint32_t mask = keep == 4 ? 0xFFFFFFFFu : (1u << (8 * keep)) - 1u;
@@ -437,10 +478,12 @@ __global__ __launch_bounds__(64 * kv_waves(D)) void kv_attn_rows_kernel(KvAttnPa
       }
     }
 
-    // running maximum and units of o
-    const float rmax = __builtin_fmaxf(__builtin_fmaxf(sv[0], sv[1]), __builtin_fmaxf(sv[2], sv[3]));
+    // running maximum and unit of o
+    f32x4 unit = sv * kv_exp_float(254 - unit_ex);
+    const float low = kv_min4(unit), top = kv_max4(unit);
+    const bool fine = kv_in_unit(low, top);
     float mx[RT];
-    bool raise = rmax > R;
+    bool raise = !fine;
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
       mx[t] = y[t][0][0];
@@ -449,16 +492,36 @@ __global__ __launch_bounds__(64 * kv_waves(D)) void kv_attn_rows_kernel(KvAttnPa
       raise = raise || mx[t] > m[t] + 8.f;
     }
     if (__ballot(raise) != 0) {
-      const float change = rmax > R ? kv_raise_unit(rmax, R, invR) : 1.f;
+      float alpha[RT];
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
         const float mn = __builtin_fmaxf(m[t], kv_col_max(mx[t]));
-        const float alpha = mn == -__builtin_inff() ? 1.f : kv_exp2(m[t] - mn);
+        alpha[t] = mn == -__builtin_inff() ? 1.f : kv_exp2(m[t] - mn);
         m[t] = mn;
-        l[t] *= alpha;
-        o_off[t] *= alpha * change;
+        l[t] *= alpha[t];
+      }
+      float change = 1.f;
+      if (__builtin_amdgcn_readfirstlane(!fine))
+        change = kv_fit_unit(
+            unit, low, top,
+            [&] {  // rows past the last one (hi 0) and those that have seen nothing have no terms
+              float most = -__builtin_inff();
 #pragma unroll
-        for (int n = 0; n < N; ++n) o[t][n] *= alpha * change;
+              for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const float term = kv_max4(y[t][i]) + __builtin_amdgcn_logf(unit[i]) - m[t];
+                  most = hi[t] > 0 && m[t] > -__builtin_inff() ? __builtin_fmaxf(most, term) : most;
+                }
+              return kv_wave_max(most);
+            },
+            unit_ex);
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        const float f = alpha[t] * change;
+        o_off[t] *= f;
+#pragma unroll
+        for (int n = 0; n < N; ++n) o[t][n] *= f;
       }
     }
     if (BYTES && k % kKvOffsetRowPages == 0) {
@@ -470,7 +533,6 @@ __global__ __launch_bounds__(64 * kv_waves(D)) void kv_attn_rows_kernel(KvAttnPa
       }
     }
     half8_t ph_[RT][2], pl_[RT][2];
-    const f32x4 unit = sv * invR;
     load_scales(next);
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
@@ -520,7 +582,7 @@ __global__ __launch_bounds__(64 * kv_waves(D)) void kv_attn_rows_kernel(KvAttnPa
   for (int t = 0; t < RT; ++t) {
     const float sum = kv_col_sum(l[t]);
 #pragma unroll
-    for (int n = 0; n < N; ++n) *reinterpret_cast<f32x4*>(lds + ((wave * N + n) * 64 + lane) * 4) = (o[t][n] - o_off[t]) * (R * kKvUnit<BYTES>);
+    for (int n = 0; n < N; ++n) *reinterpret_cast<f32x4*>(lds + ((wave * N + n) * 64 + lane) * 4) = (o[t][n] - o_off[t]) * (kv_exp_float(unit_ex) * kKvUnit<BYTES>);
     if (g == 0) *reinterpret_cast<float2*>(ml + (wave * 16 + r) * 2) = make_float2(m[t], sum);
     __syncthreads();
     const int row = 16 * t + r;  // of the tile; the same for all that a thread takes

@@ -12,9 +12,9 @@
 //
 // The probabilities are rounded to fp16 (nearest even) once, with V's block
 // scale folded in: by up to 2^-11 of each, 2^-12 on average, as the rounding of
-// the result, or by 2^-32 of the largest possible one (kKvLift).  Their sum is
-// taken of the rounded ones, so that a row that sees few tokens does not keep
-// the rounding of a common factor.
+// the result, or by 2^-32 of the outputs' unit (kKvLift, kv_in_unit).
+// Their sum is taken of the rounded ones, so that a row that sees few tokens
+// does not keep the rounding of a common factor.
 //
 // Bound by issue: a wave's page of 128 dimensions is 68 matrix instructions
 // (1090 cycles), some 210 vector instructions (1290, a quarter of them for
@@ -173,7 +173,7 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
   const float pick_off = term == 0 ? kKvOffset<BYTES> : 0.f;
   float m[2], l[2], base[2];  // base: what is taken off a score, the maximum less kKvLift, 0 while there is none
   bool fresh = true;          // some row has seen nothing yet
-  float R = 0x1p-100f, invR = 0x1p100f;
+  int unit_ex = kKvLeastUnit;  // of R, the unit of o
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     m[t] = row0 + 32 * wave + 16 * t + r < rows ? -__builtin_inff() : 0.f;
@@ -224,7 +224,7 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
           for (int i = 0; i < 4; ++i)
             if (16 * i >= held) {
               c[i] = 0.f;
-              sv[i] = held > 0 ? sv[0] : 0.f;
+              sv[i] = held > 0 ? sv[0] : kv_exp_float(unit_ex);
             }
         }
 #pragma unroll
@@ -240,24 +240,8 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
         }
         c = f32x4{1.f, 1.f, 1.f, 1.f};  // a hidden score times 0 would be no number
       }
-      // V's scales in units of R: they go into the exponent.  R is raised
-      // (and what is in its units brought along) when one passes it.
-      f32x4 unit = sv * invR;
-      if (__builtin_amdgcn_readfirstlane(kv_max3(__builtin_fmaxf(unit[0], unit[1]), unit[2], unit[3]) > 1.f)) {
-        const float change = kv_raise_unit(kv_max3(__builtin_fmaxf(sv[0], sv[1]), sv[2], sv[3]), R, invR);
-        unit = sv * invR;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          sums[t][0] *= change;
-#pragma unroll
-          for (int n = 0; n < N; ++n) {
-            kv_stay<D>(o[t][n]);
-            o[t][n] *= change;
-            kv_stay<D>(o[t][n]);
-          }
-        }
-      }
-      f32x4 log_unit;
+      // V's scales in units of R: they go into the exponent.
+      f32x4 unit = sv * kv_exp_float(254 - unit_ex), log_unit;
 #pragma unroll
       for (int i = 0; i < 4; ++i) log_unit[i] = __builtin_amdgcn_logf(unit[i]);
       half8_t pb[2][2];
@@ -273,9 +257,11 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
       // The maximum stays as it is unless a probability, in V's units, passes
       // 2^8 (2^15 as it is held): found on the packed ones, which are half as
       // many as the scores.
-      // A block of V far below the others (fine false) would hide how large
-      // the probability itself is: there the scores are looked at.
-      const bool fine = __builtin_amdgcn_readfirstlane(kv_min4(unit) >= 0x1p-6f);
+      // Where V's scales leave R's range (fine false) R is fitted to them and
+      // the scores are looked at: a block of V far below the others would hide
+      // how large the probability itself is.
+      const float low = kv_min4(unit), most_unit = kv_max4(unit);
+      bool fine = __builtin_amdgcn_readfirstlane(kv_in_unit(low, most_unit));
       // (Only then does o begin from what may be negative: until then it and
       // the offset's sum are rounded alike, and a value of 0 comes back as 0.)
       const bool take_off = BYTES && at % kKvOffsetPages == 0;
@@ -294,6 +280,7 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
       }
       if (raise) {
         fresh = false;
+        float alpha[2];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           float mx = -__builtin_inff();
@@ -303,19 +290,42 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
             mx = __builtin_fmaxf(mx, most * c[i]);
           }
           const float mn = __builtin_fmaxf(m[t], kv_col_max(mx));
-          const float alpha = mn == -__builtin_inff() ? 1.f : kv_exp2(m[t] - mn);
+          alpha[t] = mn == -__builtin_inff() ? 1.f : kv_exp2(m[t] - mn);
           m[t] = mn;
           base[t] = mn == -__builtin_inff() ? 0.f : mn - kKvLift;
           fresh = fresh || __ballot(mn == -__builtin_inff()) != 0;
-          l[t] *= alpha;
-          const float off = take_off ? sums[t][0] : 0.f;
+          l[t] *= alpha[t];
+        }
+        float change = 1.f;
+        if (!fine) {
+          change = kv_fit_unit(
+              unit, low, most_unit,
+              [&] {  // rows past the last one (hi 0) and those that have seen nothing have no terms
+                float most = -__builtin_inff();
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    const float term = kv_max4(y[t][i]) * c[i] + log_unit[i] - m[t];
+                    most = hi[t] > 0 && m[t] > -__builtin_inff() ? __builtin_fmaxf(most, term) : most;
+                  }
+                return kv_wave_max(most);
+              },
+              unit_ex);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) log_unit[i] = __builtin_amdgcn_logf(unit[i]);
+          fine = __builtin_amdgcn_readfirstlane(kv_min4(unit) >= 0x1p-6f && kv_max4(unit) <= 0x1p6f);
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const float f = alpha[t] * change, off = take_off ? sums[t][0] : 0.f;
 #pragma unroll
           for (int n = 0; n < N; ++n) {
             kv_stay<D>(o[t][n]);
-            o[t][n] = BYTES ? (o[t][n] - off) * alpha : o[t][n] * alpha;
+            o[t][n] = BYTES ? (o[t][n] - off) * f : o[t][n] * f;
             kv_stay<D>(o[t][n]);
           }
-          sums[t] = f32x4{(sums[t][0] - off) * alpha, sums[t][1] * alpha, sums[t][2] * alpha, 0.f};
+          sums[t] = f32x4{(sums[t][0] - off) * f, sums[t][1] * alpha[t], sums[t][2] * alpha[t], 0.f};
         }
         weigh();
       }
@@ -366,7 +376,7 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const float sum = kv_col_sum(l[t]) + (sums[t][1] + sums[t][2]);
-    const float unit = R * kKvUnit<BYTES>;  // of o
+    const float unit = kv_exp_float(unit_ex) * kKvUnit<BYTES>;  // of o
     const int in = 32 * wave + 16 * t + r, row = row0 + in;
     if (row >= rows) continue;
     if (w.parts == 1) {

@@ -408,9 +408,13 @@ int bq_kv_read(const bq_kv_cache* cache, int layer, void* k, void* v, const int*
  * that sees nothing gives zeros; tokens that no page holds are not seen.
  * Scores, sums and outputs in fp32, codes exact.  Up to 16 rows of a
  * key/value head and sequence on average (rows times q_heads / kv_heads; 32
- * where head_dim <= 128) the probabilities enter the product with V as sums
- * of two fp16 numbers; beyond that they are rounded to fp16 once and divided
- * by the sum of the rounded ones.
+ * where head_dim <= 128) the probabilities, times V's scale, enter the product
+ * with V as sums of two fp16 numbers; beyond that they are rounded to fp16
+ * once and divided by the sum of the rounded ones.  What a term loses is at
+ * most 2^-22 (rounded once: 2^-11) of it, or 2^-25 of the smallest scale
+ * above 0 of the term's page, or 2^-31 of the page's largest term among the
+ * rows taken together, whichever is most (times the code; a row's largest
+ * probability taken as 1).
  *
  * workspace (device memory, 16-byte aligned, or NULL): lets the tokens of a
  * long sequence be shared by several workgroups.  Its first
