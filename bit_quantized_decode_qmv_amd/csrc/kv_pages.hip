@@ -29,12 +29,14 @@ dim3 copy_grid(const KvPool& p, int64_t most) {
   return dim3((unsigned)(p.layers * 2), (unsigned)(units * pairs));
 }
 
+// entries: of the table, at most
 int check_tables(const bq_kv_cache* cache, const int* table, const int* refs, int rows, int max_pages, const int* status,
-                 const void* workspace, size_t workspace_bytes) {
+                 const void* workspace, size_t workspace_bytes, int64_t entries = INT64_MAX) {
   const int st = kv_check_cache(cache);
   if (st != BQ_OK) return st;
   if (!table || !refs || !status) return BQ_ERR_NULL;
-  if (rows < 1 || rows > (1 << 20) || max_pages < 1 || max_pages > (1 << 24)) return BQ_ERR_SHAPE;
+  if (rows < 1 || rows > (1 << 20) || max_pages < 1 || max_pages > (1 << 24) || (int64_t)rows * max_pages > entries)
+    return BQ_ERR_SHAPE;
   if (!workspace || workspace_bytes < kv_plan_ints(cache->num_pages, rows) * 4) return BQ_ERR_WORKSPACE;
   if (!kv_aligned(table, 4) || !kv_aligned(refs, 4) || !kv_aligned(status, 4) || !kv_aligned(workspace, 16))
     return BQ_ERR_ALIGN;
@@ -96,7 +98,8 @@ int bq_kv_fork(const bq_kv_cache* cache, int* table, int* lens, int* refs, int r
 
 int bq_kv_resize(const bq_kv_cache* cache, int* table, int* lens, int* refs, int rows, int max_pages, const int* want,
                  int* status, void* workspace, size_t workspace_bytes, void* stream) {
-  const int st = check_tables(cache, table, refs, rows, max_pages, status, workspace, workspace_bytes);
+  // the plan counts the pages that all rows ask for in 31 bits
+  const int st = check_tables(cache, table, refs, rows, max_pages, status, workspace, workspace_bytes, INT32_MAX);
   if (st != BQ_OK) return st;
   if (!lens || !want) return BQ_ERR_NULL;
   if (!kv_aligned(lens, 4) || !kv_aligned(want, 4)) return BQ_ERR_ALIGN;

@@ -451,6 +451,7 @@ int bq_kv_attn(const bq_kv_cache* cache, int layer, const void* q, void* out, lo
  *            Shorter: pages past it are let go, and a last page that is then
  *            partly filled and still shared is copied.  Longer: pages are
  *            taken; their contents are undefined until written.
+ *            rows * max_pages < 2^31.
  * kv_compact moves pages so that those in use have the lowest ids: the ids in
  *            use from their number on, ascending, go to the free ids below
  *            it, ascending; table and refs follow.
