@@ -394,9 +394,12 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvReadParams p) {
   if (!kv_locate(p.batch, item, count, s, b, local)) return;
   const int pages = kv_touched(s, first);
   if (local == pages) {
-    for (int i = (int)threadIdx.x; i < (s.n - s.len) * units * 2; i += 256) {
-      const int which = i & 1, u = (i >> 1) % units, row = s.q0 + (i >> 1) / units;
-      half8_t* o = reinterpret_cast<half8_t*>((which ? p.ov : p.ok) + ((int64_t)row * p.kv_heads + head) * D + u * 16);
+    // by rows: 2 units of each are more than 31 bits count
+    const int at_once = 256 / (2 * units), first_row = (int)threadIdx.x / (2 * units);
+    const int in = (int)threadIdx.x - first_row * 2 * units, which = in & 1, u = in >> 1;
+    if (first_row >= at_once) return;
+    for (int row = first_row; row < s.n - s.len; row += at_once) {
+      half8_t* o = reinterpret_cast<half8_t*>((which ? p.ov : p.ok) + ((int64_t)(s.q0 + row) * p.kv_heads + head) * D + u * 16);
       o[0] = o[1] = half8_t{};
     }
     return;
