@@ -267,6 +267,17 @@ def _stream_handle(device):
     return torch.cuda.current_stream(device).cuda_stream
 
 
+def _launch(device, entry, *args):
+    """entry(*args, stream) on the current stream of the tensors' device, with
+    that device current: the default stream's handle is 0 on every device, and
+    a launch on it goes to the current one."""
+    torch = _torch()
+    if torch.cuda.current_device() == device.index:
+        return entry(*args, _stream_handle(device))
+    with torch.cuda.device(device):
+        return entry(*args, _stream_handle(device))
+
+
 def _run(name, x, w, scales, biases, bits, group_size, out, M, N, K, out_shape):
     torch = _torch()
     dev = w.device
@@ -282,9 +293,8 @@ def _run(name, x, w, scales, biases, bits, group_size, out, M, N, K, out_shape):
         _check(out, "out", torch.float16, dev)
         if tuple(out.shape) != tuple(out_shape):
             raise ValueError(f"out has shape {tuple(out.shape)}, expected {tuple(out_shape)}")
-    _call(name, x.data_ptr() if x is not None else None, w.data_ptr(), scales.data_ptr(),
-          biases.data_ptr() if biases is not None else None, out.data_ptr(), M, N, K, bits,
-          group_size, _stream_handle(dev))
+    _launch(dev, _call, name, x.data_ptr() if x is not None else None, w.data_ptr(), scales.data_ptr(),
+            biases.data_ptr() if biases is not None else None, out.data_ptr(), M, N, K, bits, group_size)
     return out
 
 
@@ -360,9 +370,9 @@ def _run_ws(name, x, w, scales, biases, bits, group_size, out, workspace):
     elif workspace.device != dev:
         raise ValueError(f"workspace is on {workspace.device}, expected {dev}")
     fn = bq_t5_qmm_ws if name == "bq_t5_qmm_ws" else bq_qmm_ws
-    fn(x.data_ptr(), w.data_ptr(), scales.data_ptr(), biases.data_ptr() if biases is not None else None,
-       out.data_ptr(), M, N, K, bits, group_size, workspace.data_ptr() if workspace is not None else None,
-       workspace.numel() * workspace.element_size() if workspace is not None else 0, _stream_handle(dev))
+    _launch(dev, fn, x.data_ptr(), w.data_ptr(), scales.data_ptr(), biases.data_ptr() if biases is not None else None,
+            out.data_ptr(), M, N, K, bits, group_size, workspace.data_ptr() if workspace is not None else None,
+            workspace.numel() * workspace.element_size() if workspace is not None else 0)
     return out
 
 
@@ -394,8 +404,7 @@ def sym_check(scales, biases, bits: int, group_size: int) -> bool:
         raise ValueError("scales and biases must have the same shape")
     N, G = scales.shape
     flag = torch.empty(1, dtype=torch.int32, device=dev)
-    bq_sym_check(scales.data_ptr(), biases.data_ptr(), N, G * group_size, bits, group_size, flag.data_ptr(),
-                 _stream_handle(dev))
+    _launch(dev, bq_sym_check, scales.data_ptr(), biases.data_ptr(), N, G * group_size, bits, group_size, flag.data_ptr())
     return bool(flag.item())
 
 
@@ -411,7 +420,7 @@ def t5_repack(w, bits: int, group_size: int, K: int):
         raise ValueError(f"w has shape {tuple(w.shape)}, expected ({N}, {K * bits // 32})")
     out = torch.empty((N, (K // group_size) * ((group_size + 4) // 5)), dtype=torch.uint8, device=dev)
     flag = torch.empty(1, dtype=torch.int32, device=dev)
-    bq_t5_repack(w.data_ptr(), out.data_ptr(), N, K, bits, group_size, flag.data_ptr(), _stream_handle(dev))
+    _launch(dev, bq_t5_repack, w.data_ptr(), out.data_ptr(), N, K, bits, group_size, flag.data_ptr())
     return out, bool(flag.item())
 
 
@@ -441,10 +450,9 @@ def spec_decode_verify(logits, draft, workspace=None, targets: bool = True):
     accepted = torch.empty(B, dtype=torch.int32, device=dev)
     nxt = torch.empty(B, dtype=torch.int32, device=dev)
     tgt = torch.empty((B, rows), dtype=torch.int32, device=dev) if targets else None
-    bq_spec_decode_verify(logits.data_ptr(), DTYPE_F16 if logits.dtype == torch.float16 else DTYPE_F32,
-                          draft.data_ptr() if L > 0 else None, B, L, V, accepted.data_ptr(), nxt.data_ptr(),
-                          tgt.data_ptr() if tgt is not None else None, workspace.data_ptr(), workspace.numel(),
-                          _stream_handle(dev))
+    _launch(dev, bq_spec_decode_verify, logits.data_ptr(), DTYPE_F16 if logits.dtype == torch.float16 else DTYPE_F32,
+            draft.data_ptr() if L > 0 else None, B, L, V, accepted.data_ptr(), nxt.data_ptr(),
+            tgt.data_ptr() if tgt is not None else None, workspace.data_ptr(), workspace.numel())
     return accepted, nxt, tgt
 
 
@@ -514,7 +522,7 @@ def linear(x, qw: QuantizedWeight, out=None, sym: Optional[bool] = None, workspa
             qw.biases.data_ptr() if qw.biases is not None else None, out.data_ptr(), M, qw.N, qw.K, qw.bits,
             qw.group_size, LINEAR_SYM if use_sym else 0)
     if workspace is None:
-        bq_linear(*args, _stream_handle(dev))
+        _launch(dev, bq_linear, *args)
         return out
     if isinstance(workspace, str):
         if workspace != "auto":
@@ -523,7 +531,7 @@ def linear(x, qw: QuantizedWeight, out=None, sym: Optional[bool] = None, workspa
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
     elif workspace.device != dev:
         raise ValueError(f"workspace is on {workspace.device}, expected {dev}")
-    bq_linear_ws(*args, workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream_handle(dev))
+    _launch(dev, bq_linear_ws, *args, workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out
 
 

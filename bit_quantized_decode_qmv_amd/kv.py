@@ -61,14 +61,16 @@ def declare(lib) -> None:
 _bq = sys.modules[__package__]
 _torch = None
 _raw_stream = None
+_device_now = None
 
 
 def _use_torch():
-    global _torch, _raw_stream
+    global _torch, _raw_stream, _device_now
     import torch
-    # the current stream's handle by itself where torch offers it: a call's
-    # host time is a few microseconds in all
+    # the current stream's handle and device by themselves where torch offers
+    # them: a call's host time is a few microseconds in all
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _device_now = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
     _torch = torch
     return torch
 
@@ -95,6 +97,15 @@ def _call(name, *args):
     if st < 0:
         raise _bq.BQError(st, lib.bq_strerror(st).decode(), name)
     return st
+
+
+def _launch(device, name, *args):
+    """The entry point on the current stream of the tensors' device, with that
+    device current (as the package's _launch)."""
+    if _device_now() == device.index:
+        return _call(name, *args, _stream(device))
+    with _torch.cuda.device(device):
+        return _call(name, *args, _stream(device))
 
 
 def _c_entry(name):
@@ -262,7 +273,7 @@ def rope(x, pos, inv_freq, axis=None, adjacent: bool = False, out=None):
     tokens, heads, dim = x.shape
     a = _angles(pos, inv_freq, axis, adjacent, tokens, dev)
     out, out_stride = _out(out, "out", x, dev)
-    _call("bq_rope", x.data_ptr(), out.data_ptr(), stride, out_stride, tokens, heads, dim, *a, _stream(dev))
+    _launch(dev, "bq_rope", x.data_ptr(), out.data_ptr(), stride, out_stride, tokens, heads, dim, *a)
     return out
 
 
@@ -286,9 +297,8 @@ def kv_append(cache: KVCache, layer: int, k, v, cu, lens, table, q=None, pos=Non
             raise ValueError(f"q has {q.shape[0]} rows, k {total}")
         q_out, out_stride = _out(q_out, "q_out", q, dev)
         qp, op, q_heads = q.data_ptr(), q_out.data_ptr(), q.shape[1]
-    _call("bq_kv_append", cache.desc, layer, k.data_ptr(), v.data_ptr(), k_stride, v_stride, qp, op, q_stride,
-          out_stride, q_heads, cu.data_ptr(), lens.data_ptr(), table.data_ptr(), batch, max_pages, total, *a,
-          _stream(dev))
+    _launch(dev, "bq_kv_append", cache.desc, layer, k.data_ptr(), v.data_ptr(), k_stride, v_stride, qp, op, q_stride,
+            out_stride, q_heads, cu.data_ptr(), lens.data_ptr(), table.data_ptr(), batch, max_pages, total, *a)
     return q_out if q is not None else None
 
 
@@ -298,8 +308,8 @@ def kv_read(cache: KVCache, layer: int, cu, lens, table, total: int):
     dev = cache.device
     batch, max_pages = _batch(cu, lens, table, dev)
     k, v = (_torch.empty((total, cache.kv_heads, cache.head_dim), dtype=_torch.float16, device=dev) for _ in range(2))
-    _call("bq_kv_read", cache.desc, layer, k.data_ptr(), v.data_ptr(), cu.data_ptr(), lens.data_ptr(),
-          table.data_ptr(), batch, max_pages, total, _stream(dev))
+    _launch(dev, "bq_kv_read", cache.desc, layer, k.data_ptr(), v.data_ptr(), cu.data_ptr(), lens.data_ptr(),
+            table.data_ptr(), batch, max_pages, total)
     return k, v
 
 
@@ -325,9 +335,9 @@ def kv_attn(cache: KVCache, layer: int, q, cu, lens, table, scale: Optional[floa
         ws_bytes = workspace.numel()
     if workspace is not None:
         ws = workspace.data_ptr()
-    _call("bq_kv_attn", cache.desc, layer, q.data_ptr(), out.data_ptr(), stride, out_stride, heads, cu.data_ptr(),
-          lens.data_ptr(), table.data_ptr(), batch, max_pages, total, dim ** -0.5 if scale is None else scale, window,
-          KV_CAUSAL if causal else 0, ws, ws_bytes, _stream(dev))
+    _launch(dev, "bq_kv_attn", cache.desc, layer, q.data_ptr(), out.data_ptr(), stride, out_stride, heads, cu.data_ptr(),
+            lens.data_ptr(), table.data_ptr(), batch, max_pages, total, dim ** -0.5 if scale is None else scale, window,
+            KV_CAUSAL if causal else 0, ws, ws_bytes)
     return out
 
 
@@ -351,8 +361,8 @@ def _page_call(name, cache, table, refs, workspace, before, after):
     else:
         _need(workspace, "workspace", _torch.uint8, dev)
         size = workspace.numel()
-    _call(name, cache.desc, table.data_ptr(), *before, refs.data_ptr(), rows, max_pages, *after, status.data_ptr(),
-          workspace.data_ptr(), size, _stream(dev))
+    _launch(dev, name, cache.desc, table.data_ptr(), *before, refs.data_ptr(), rows, max_pages, *after,
+            status.data_ptr(), workspace.data_ptr(), size)
     return status
 
 
@@ -401,7 +411,7 @@ def kv_copy_pages(cache: KVCache, src, dst) -> None:
     n = src.shape[0]
     _ints(src, "src", dev, n)
     _ints(dst, "dst", dev, n)
-    _call("bq_kv_copy_pages", cache.desc, src.data_ptr(), dst.data_ptr(), n, _stream(dev))
+    _launch(dev, "bq_kv_copy_pages", cache.desc, src.data_ptr(), dst.data_ptr(), n)
 
 
 __all__ = [

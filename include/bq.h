@@ -30,6 +30,7 @@
  *   group_size  64 or 128.
  *   stream  a hipStream_t (NULL = the default stream).  Every call only
  *           enqueues work on it and returns; there is no synchronization.
+ *           The current HIP device has to be the stream's and the pointers'.
  *
  * Ownership: all pointers are device pointers owned by the caller.  The
  * library allocates nothing per call and keeps no mutable global state,
