@@ -189,6 +189,13 @@ class KVCache:
                    *(torch.empty(scales, dtype=torch.float32, device=device) for _ in range(2)), format=format)
 
 
+def _int(value, name) -> int:
+    """A number as the C entry points hold it; ctypes would drop the bits past the 32nd."""
+    if not -1 << 31 <= value < 1 << 31:
+        raise ValueError(f"{name} = {value} does not fit 32 bits")
+    return value
+
+
 def _rows(t, name, device, heads=None, head_dim=None):
     """Checks a row array [tokens][heads][head_dim], fp16, any row stride; returns its row stride."""
     torch = _torch or _use_torch()
@@ -204,6 +211,7 @@ def _rows(t, name, device, heads=None, head_dim=None):
     if len(shape) != 3 or (heads is not None and shape[1] != heads) or (head_dim is not None and shape[2] != head_dim):
         raise ValueError(f"{name} has shape {tuple(shape)}, expected [tokens][{heads or 'heads'}][{head_dim or 'head_dim'}]")
     n, h, d = shape
+    _int(n, f"the rows of {name}")
     s0, s1, s2 = t.stride()
     row = h * d
     if s2 != 1 or (s1 != d and h > 1):
@@ -297,8 +305,8 @@ def kv_append(cache: KVCache, layer: int, k, v, cu, lens, table, q=None, pos=Non
             raise ValueError(f"q has {q.shape[0]} rows, k {total}")
         q_out, out_stride = _out(q_out, "q_out", q, dev)
         qp, op, q_heads = q.data_ptr(), q_out.data_ptr(), q.shape[1]
-    _launch(dev, "bq_kv_append", cache.desc, layer, k.data_ptr(), v.data_ptr(), k_stride, v_stride, qp, op, q_stride,
-            out_stride, q_heads, cu.data_ptr(), lens.data_ptr(), table.data_ptr(), batch, max_pages, total, *a)
+    _launch(dev, "bq_kv_append", cache.desc, _int(layer, "layer"), k.data_ptr(), v.data_ptr(), k_stride, v_stride, qp, op,
+            q_stride, out_stride, q_heads, cu.data_ptr(), lens.data_ptr(), table.data_ptr(), batch, max_pages, total, *a)
     return q_out if q is not None else None
 
 
@@ -307,8 +315,9 @@ def kv_read(cache: KVCache, layer: int, cu, lens, table, total: int):
     cu[b+1] - cu[b] tokens of each sequence; total = cu[-1]."""
     dev = cache.device
     batch, max_pages = _batch(cu, lens, table, dev)
+    _int(total, "total")
     k, v = (_torch.empty((total, cache.kv_heads, cache.head_dim), dtype=_torch.float16, device=dev) for _ in range(2))
-    _launch(dev, "bq_kv_read", cache.desc, layer, k.data_ptr(), v.data_ptr(), cu.data_ptr(), lens.data_ptr(),
+    _launch(dev, "bq_kv_read", cache.desc, _int(layer, "layer"), k.data_ptr(), v.data_ptr(), cu.data_ptr(), lens.data_ptr(),
             table.data_ptr(), batch, max_pages, total)
     return k, v
 
@@ -335,9 +344,9 @@ def kv_attn(cache: KVCache, layer: int, q, cu, lens, table, scale: Optional[floa
         ws_bytes = workspace.numel()
     if workspace is not None:
         ws = workspace.data_ptr()
-    _launch(dev, "bq_kv_attn", cache.desc, layer, q.data_ptr(), out.data_ptr(), stride, out_stride, heads, cu.data_ptr(),
-            lens.data_ptr(), table.data_ptr(), batch, max_pages, total, dim ** -0.5 if scale is None else scale, window,
-            KV_CAUSAL if causal else 0, ws, ws_bytes)
+    _launch(dev, "bq_kv_attn", cache.desc, _int(layer, "layer"), q.data_ptr(), out.data_ptr(), stride, out_stride, heads,
+            cu.data_ptr(), lens.data_ptr(), table.data_ptr(), batch, max_pages, total, dim ** -0.5 if scale is None else scale,
+            _int(min(window, (1 << 31) - 1), "window"), KV_CAUSAL if causal else 0, ws, ws_bytes)
     return out
 
 
