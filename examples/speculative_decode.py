@@ -116,7 +116,8 @@ def decode(session, prompt, samples, steps, draft_len, seed=0, compact=True):
     counts = ints([prompt.numel()] + [0] * (rows - 1))
     logits = session.feed(prompt, counts)
     first = int(logits[-1].float().argmax())
-    session.fork([0] * (samples - 1), list(range(1, samples)))
+    if samples > 1:
+        session.fork([0] * (samples - 1), list(range(1, samples)))
     counts = ints([draft_len + 1] * samples + [0] * (rows - samples))
     # each sample goes on from a token of its own
     last = (torch.arange(samples, device="cuda", dtype=torch.int32) + first) % vocab
