@@ -38,8 +38,9 @@ const void* pick_join(int D) {
 
 // Few rows: workgroups to aim at, one for each CU, whose registers one fills.
 // Parts beyond that (twice, three times as many) measured slower on every
-// batch: a part costs some 8 us of its own.  From kRowTiles workgroups on no
-// tile is split.
+// batch: with one workgroup on a CU, its start (batch, table, first page) and
+// its join, some 8 us, overlap with nobody's loads.  From kRowTiles workgroups
+// on no tile is split.
 constexpr int kTarget = 256, kRowTiles = 4096;
 constexpr int kCounters = BQ_KV_ATTN_COUNTER_BYTES / 4;
 
@@ -56,7 +57,7 @@ Plan plan(const bq_kv_cache* c, int q_heads, int batch, int total, int64_t max_p
   // not fit a wave's registers.  Tiles of 32 for up to 128 rows instead:
   // 6 x 77 rows over 1500 tokens, 16 heads of 64, 17.9 us against 16.1, 24
   // times 41.4 against 33.3, 8 x 96 rows over 4000, heads of 128, 31.7 against
-  // 27.0; over 8000 tokens 34.3 against 37.4.
+  // 27.0; over 8000 tokens 34.3 against 37.4 (the length is not looked at).
   const int64_t rows = (int64_t)total * (q_heads / c->kv_heads);
   const bool narrow = c->head_dim <= 128;
   p.rows = rows <= 16 * (int64_t)batch ? 16 : narrow && rows <= 32 * (int64_t)batch ? 32 : kPromptRows;
@@ -145,7 +146,10 @@ int bq_kv_attn(const bq_kv_cache* cache, int layer, const void* q, void* out, lo
   const Plan pl = plan(cache, q_heads, batch, total, max_pages, workspace ? workspace_bytes : 0);
   p.target = (int)pl.target;
   // (many rows, measured: parts of 4 pages are 17% faster than of 8 at D 64,
-  // 13% slower at D 128)
+  // 13% slower at D 128.  Wide heads, 4 with 6 query heads each, us in parts of
+  // 4, 8 and 16 pages: 40 rows of 2 sequences of up to 4000 tokens, D 256, 34.2,
+  // 39.8 and 56.1, D 192 29.3, 33.5 and 47.2; 100 rows over 8000, D 256, 66.5,
+  // 66.5 and 60.1; five rows of 8 sequences of up to 16000 67.5, 67.5 and 58.3)
   p.min_pages = pl.rows < kPromptRows ? 0 : D == 64 ? 4 : 8;
   p.counters = static_cast<unsigned*>(workspace);
   p.part = workspace ? reinterpret_cast<float*>(static_cast<char*>(workspace) + BQ_KV_ATTN_COUNTER_BYTES) : nullptr;

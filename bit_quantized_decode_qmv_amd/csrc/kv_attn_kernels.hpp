@@ -174,16 +174,26 @@ __device__ __forceinline__ bool kv_attn_work(const KvAttnParams& p, int item, Kv
     for (int base = 0; base < batch; base += 64) all += tiles(seq(base)) * pages(seq(base));
     if (__ballot(falls) != 0) return false;
     all = __builtin_amdgcn_readlane(kv_scan(all), 63);
-    // few rows: no part shorter than pays for joining it (measured, one
-    // sequence, 8 heads of 128: 16 pages 10.0 us in one part and 11.9 in two;
-    // 32 pages 14.4 us in parts of 16 and 11.9 in parts of 8; 2047 pages of
-    // one head 28.6 us in parts of 16 and 41.1 in parts of 8)
+    // few rows: no part shorter than pays for joining it.  Measured, heads of
+    // 128, us in parts of 16 pages at least and of 8:
+    //   one sequence, 8 heads: 16 pages 9.5 and 12.0, 17 13.5 and 11.6, 32 13.8
+    //   and 12.0, 64 13.8 and 12.2, 65 13.6 and 12.2, 128 15.2 and 14.7, 256
+    //   16.4 and 18.9, 400 20.0 and 20.3;
+    //   one head: 65 13.5 and 11.7, 128 13.6 and 11.7, 256 13.7 and 13.9, 400
+    //   15.8 and 17.4;
+    //   8 heads, two sequences of 16 pages 9.6 and 12.0, of 64 15.1 and 14.0,
+    //   four of 64 15.9 and 16.0.
+    // The rule goes by the pages of all tiles together, which is coarse: it
+    // gives away some 2 us from 65 to about 128 pages, and where several
+    // sequences of up to 16 pages are 64 together or fewer.
     const int least = p.min_pages > 0 ? p.min_pages : all <= 16 || all > 64 ? 16 : 8;
     // A quarter more than an even share, few rows: every tile's last part comes
     // on top of the whole ones, and would run in a second round.  Measured, 8
     // heads of 128, even shares and a quarter more: 4 sequences of up to 30000
     // tokens 31.4 us and 24.4, 16 of up to 16000 47.9 and 41.2, 64 of up to
     // 4100 44.6 and 41.7; five rows each of 32 of up to 16384 87.9 and 89.2.
+    // (Where all shares fit one round there is nothing to gain: one head over
+    // 2047 pages has parts of 20 pages, 103 of them, 26 us.)
     const unsigned share = ROWS <= 32 ? (unsigned)all + (unsigned)all / 4 : (unsigned)all;
     w.chunk = max((int)((share + p.target - 1) / (unsigned)p.target), least);
   }
@@ -328,8 +338,9 @@ constexpr int kv_waves(int D) { return D <= 128 ? 8 : 4; }
 //
 // Measured, 8 heads of 128 with 6 query heads each: one row over 131001
 // tokens 55 us (4.9 TB/s of codes), over 1003 tokens 9.6 us (a launch, the
-// table, one page a wave and the join); five rows each of 32 sequences of
-// 1024 to 16384 tokens (e4m3) 87 us (4.3 TB/s).
+// table, two pages a wave and the join); one row each of 16 sequences of 1000
+// to 16000 tokens 41 us; five rows each of 32 sequences of 1024 to 16384
+// tokens (e4m3) 88 us (4.3 TB/s).
 template <int D, int FMT, int RT>
 __global__ __launch_bounds__(64 * kv_waves(D)) void kv_attn_rows_kernel(KvAttnParams p) {
   constexpr int C = D / 64, N = D / 16, ROWS = 16 * RT, NW = kv_waves(D), THREADS = 64 * NW;

@@ -17,13 +17,14 @@
 // does not keep the rounding of a common factor.
 //
 // Bound by issue: a wave's page of 128 dimensions is 68 matrix instructions
-// (1090 cycles), some 210 vector instructions (1290, a quarter of them for
+// (1090 cycles), some 220 vector instructions (1350, a quarter of them for
 // the exponentials) and 32 reads of LDS (256 of the CU's), of two waves a
 // SIMD.  Measured: 2047 rows of 48 heads (8 of them keys' and values') of 128
-// over 10240 tokens 484 us, 0.96 PFLOP/s; the matrix instructions alone 200,
-// without the softmax 334.  One wave a SIMD with 64 rows reads LDS half as
-// often, and took 714 us; eight waves with 256 rows 474 before other steps,
-// but 10 to 40% more where prompts are short.
+// over 10240 tokens 485 us, 0.96 PFLOP/s, in a run of calls (the first ten
+// after a pause take up to 620, and the time falls over the next fifty); the
+// matrix instructions alone 200, without the softmax 334.  One wave a SIMD with
+// 64 rows reads LDS half as often, and took 714 us; eight waves with 256 rows
+// 474 before other steps, but 10 to 40% more where prompts are short.
 #pragma once
 
 #include "kv_attn_kernels.hpp"

@@ -367,7 +367,8 @@ typedef struct bq_kv_cache {
  * BQ_ROPE_ADJACENT; dimensions past rot_dim pass through.
  * x, y: rows as above, y may be x (with the same stride); head_dim a multiple of 16 up to
  * 1024, rot_dim a multiple of 16 up to head_dim (0: nothing turns, the
- * arrays may be NULL); pos int32 [axes][tokens], inv_freq fp32
+ * arrays may be NULL); up to 2^24 tokens fit any launch, a call that does not
+ * is BQ_ERR_SHAPE; pos int32 [axes][tokens], inv_freq fp32
  * [rot_dim/2], axis int32 [rot_dim/2] (NULL: all 0; values outside 0 ..
  * axes - 1 are brought into it), 1 <= axes <= BQ_ROPE_MAX_AXES.  The angle
  * is exact to 2^-20 turns at any position.  Undefined flag bits:
