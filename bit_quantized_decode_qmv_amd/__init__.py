@@ -15,8 +15,9 @@ Two layers:
   with its symmetric-bias check done once.
 
 Attention with a paged 8-bit key/value cache (``KVCache``, ``rope``,
-``kv_append``, ``kv_attn``, ``kv_fork``, ...) is in :mod:`.kv`, whose names
-this module exports too.
+``kv_append``, ``kv_attn``, ``kv_fork``, ...) is in :mod:`.kv`, trees of
+drafted tokens and log probabilities (``tree_plan``, ``tree_accept``,
+``logprobs``) in :mod:`.draft`, whose names this module exports too.
 
 The library is loaded on first use; a missing build or an ABI mismatch is an
 error (there is no fallback path).
@@ -28,7 +29,9 @@ import os
 from typing import Optional
 
 from . import kv as _kv
+from . import draft as _draft
 from .kv import *  # noqa: F401,F403
+from .draft import *  # noqa: F401,F403
 
 ABI_VERSION = 10
 BITS_T5 = 0
@@ -53,7 +56,7 @@ ENTRY_POINTS = ("bq_qmv", "bq_qmv_wide", "bq_qmv_sym", "bq_t5_qmv", "bq_t5_qmv_w
 DISPATCH_POINTS = ("bq_linear", "bq_linear_route", "bq_sym_check", "bq_t5_repack", "bq_spec_verify_workspace",
                    "bq_spec_decode_verify", "bq_spec_decode_verify_noalloc", "bq_qmm_workspace", "bq_t5_qmm_ws",
                    "bq_qmm_ws", "bq_linear_ws")
-ALL_SYMBOLS = ("bq_abi_version", "bq_strerror") + ENTRY_POINTS + DISPATCH_POINTS + _kv.KV_POINTS
+ALL_SYMBOLS = ("bq_abi_version", "bq_strerror") + ENTRY_POINTS + DISPATCH_POINTS + _kv.KV_POINTS + _draft.DRAFT_POINTS
 
 STATUS = {
     0: "BQ_OK", -1: "BQ_ERR_NULL", -2: "BQ_ERR_BITS", -3: "BQ_ERR_GROUP", -4: "BQ_ERR_SHAPE",
@@ -116,10 +119,11 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     if ver != ABI_VERSION:
         raise ImportError(f"{p} has ABI version {ver}, this binding needs {ABI_VERSION}")
     # the cache entry points joined this ABI version: a library without them was built before
-    missing = [name for name in _kv.KV_POINTS if not hasattr(lib, name)]
+    missing = [name for name in _kv.KV_POINTS + _draft.DRAFT_POINTS if not hasattr(lib, name)]
     if missing:
         raise ImportError(f"{p} lacks {', '.join(missing)}; run __graft_entry__.build()")
     _kv.declare(lib)
+    _draft.declare(lib)
     if path is None:
         _lib = lib
     return lib
@@ -544,4 +548,4 @@ __all__ = [
     "bq_spec_verify_workspace", "bq_qmm_workspace", "bq_qmm_ws", "bq_t5_qmm_ws", "qmm_ws", "t5_qmm_ws",
     "bq_linear_ws",
     "bq_t5_repack", "spec_decode_verify", "strerror", "sym_check", "t5_qmm", "t5_qmv", "t5_qmv_wide", "t5_repack",
-] + _kv.__all__
+] + _kv.__all__ + _draft.__all__

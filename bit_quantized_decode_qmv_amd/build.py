@@ -17,7 +17,7 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG_DIR, "libbq.so")
 SOURCES = ["bq_api.hip", "qmv_u1.hip", "qmv_u2.hip", "qmv_t5.hip", "qmm_u1.hip", "qmm_u2.hip", "qmm_t5.hip",
-           "kv_cache.hip", "kv_attn.hip", "kv_pages.hip"]
+           "kv_cache.hip", "kv_attn.hip", "kv_attn_more.hip", "kv_pages.hip", "tree.hip", "logprobs.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

@@ -11,7 +11,18 @@
 // sequence's rows form one list of rows (token-major), taken 16 at a time as
 // the columns of both products:
 //   S^T [64 tokens][16 rows] = K [64][D] x Q^T,   O^T [D][16] += V^T [D][64] x P^T.
+//
+// Two more kinds of rows share these kernels (KvAttnMore): a window with
+// sinks, where a row sees the first `sinks` tokens beside those of its window,
+// and a tree of drafted tokens, where the sequence's last n tokens are seen by
+// a row as its bits say and the context ahead of them as by a window.  A tile
+// then walks the pages of the sinks and those from its first window on, as one
+// run of numbers; what differs between its rows is the masking of the pages
+// that some row does not see whole: a row's 64 bits of such a page instead of
+// one range.
 #pragma once
+
+#include <type_traits>
 
 #include "kv_common.hpp"
 
@@ -31,6 +42,11 @@ struct KvAttnParams {
   int target;            // workgroups of a head to aim at; 0: tiles are not split
   int min_pages;         // of a part; 0: by the number of pages
   int item0;             // share of the launch's first workgroups
+};
+
+struct KvAttnMore : KvAttnParams {
+  const uint64_t* mask;  // [total][words]: the rows of its sequence's tree that a row sees; null: causal
+  int words, sinks;
 };
 
 constexpr int kKvMaxParts = 128;  // of a tile
@@ -143,18 +159,24 @@ struct KvWork {
   int b, tile, split, parts, chunk;
   int slot;  // place of the tile's part 0 when the parts are kept tile by tile
 };
-__device__ __forceinline__ int kv_first_page(const KvAttnParams& p, const KvSeq& s) {
-  return p.causal && p.window > 0 ? max(s.len - s.n - p.window + 1, 0) / kKvPage : 0;
+// Pages of a sequence's tiles, at most.
+__device__ __forceinline__ int kv_pages(const KvAttnParams& p, const KvSeq& s) {
+  const int first = p.causal && p.window > 0 ? max(s.len - s.n - p.window + 1, 0) / kKvPage : 0;
+  return max((s.len + kKvPage - 1) / kKvPage - first, 1);
+}
+__device__ __forceinline__ int kv_pages(const KvAttnMore& p, const KvSeq& s) {
+  // (a row of a tree that sees none of it sees the whole window of the context)
+  const int first = p.window > 0 ? max(s.len - s.n - p.window + (p.mask ? 0 : 1), 0) / kKvPage : 0;
+  const int front = min((min(p.sinks, s.len) + kKvPage - 1) / kKvPage, first);
+  return max((s.len + kKvPage - 1) / kKvPage - first + front, 1);
 }
 // Every wave of the grid finds its share from the batch's arrays: a lane
 // takes a sequence (64 at a time; the first 64 stay in its registers).
 // JOIN: share `item` is the last part of tile `item`.
-template <int ROWS, bool JOIN = false>
-__device__ __forceinline__ bool kv_attn_work(const KvAttnParams& p, int item, KvWork& w) {
+template <int ROWS, bool JOIN = false, typename P>
+__device__ __forceinline__ bool kv_attn_work(const P& p, int item, KvWork& w) {
   const int lane = (int)threadIdx.x & 63, batch = p.batch.batch;
-  const auto pages = [&](const KvSeq& s) {
-    return max((s.len + kKvPage - 1) / kKvPage - kv_first_page(p, s), 1);
-  };
+  const auto pages = [&](const KvSeq& s) { return kv_pages(p, s); };
   const auto tiles = [&](const KvSeq& s) { return (s.n * p.group + ROWS - 1) / ROWS; };
   // Offsets that fall would make the list longer than the launch and the
   // workspace are made for: then there is no work.
@@ -265,6 +287,91 @@ __device__ __forceinline__ KvRowRange kv_row_range(const KvAttnParams& p, const 
   return r;
 }
 
+// Of rows from token t0 to token t1 of a sequence's: no row sees tokens ahead
+// of kv_first_range's lo (its sinks apart) or from kv_last_range's hi on; all
+// see those from the last's lo to the first's hi.
+__device__ __forceinline__ KvRowRange kv_first_range(const KvAttnParams& p, const KvSeq& s, int t0) { return kv_row_range(p, s, t0); }
+__device__ __forceinline__ KvRowRange kv_last_range(const KvAttnParams& p, const KvSeq& s, int t1) { return kv_row_range(p, s, t1); }
+__device__ __forceinline__ KvRowRange kv_first_range(const KvAttnMore& p, const KvSeq& s, int t0) {
+  if (!p.mask) return kv_row_range(p, s, t0);
+  const int base = s.len - s.n;
+  return KvRowRange{p.window > 0 ? max(base - p.window, 0) : 0, max(base, 0)};
+}
+__device__ __forceinline__ KvRowRange kv_last_range(const KvAttnMore& p, const KvSeq& s, int t1) {
+  if (!p.mask) return kv_row_range(p, s, t1);
+  return KvRowRange{p.window > 0 ? max(s.len - s.n - max(p.window - s.n, 0), 0) : 0, s.len};
+}
+// A tile's pages where sinks may stand apart, as places 0, 1, ..: the first
+// `front` are the sinks' pages, the others `gap` further.
+struct KvPlaces {
+  int front, gap;
+  __device__ __forceinline__ int operator()(int at) const { return at < front ? at : at + gap; }
+};
+__device__ __forceinline__ KvPlaces kv_places(const KvAttnMore& p, const KvRowRange& r0, const KvRowRange& r1) {
+  const int first = r0.lo / kKvPage, front = min((min(p.sinks, r1.hi) + kKvPage - 1) / kKvPage, first);
+  return KvPlaces{front, first - front};
+}
+__device__ __forceinline__ int kv_sinks(const KvAttnMore& p, int hi) { return min(p.sinks, hi); }
+__device__ __forceinline__ int kv_sinks(const KvAttnParams&, int) { return 0; }
+
+// Bits from up to (not including) to, of 64.
+__device__ __forceinline__ uint64_t kv_bits(int from, int to) {
+  from = max(from, 0);
+  to = min(to, 64);
+  return from < to ? (~0ull >> (64 - to + from)) << from : 0ull;
+}
+// What a row sees: the context's tokens [lo, hi) and those ahead of sinks, and
+// of a tree the rows that its words say.
+struct KvRowMore {
+  int lo, hi, sinks;
+  const uint64_t* mask;  // null: no tree (or no row)
+};
+__device__ __forceinline__ KvRowMore kv_row_more(const KvAttnMore& p, const KvSeq& s, int token, bool ok) {
+  KvRowMore r;
+  if (p.mask) {
+    const int base = s.len - s.n;
+    r.mask = ok ? p.mask + (int64_t)(s.q0 + token) * p.words : nullptr;
+    r.lo = 0;
+    if (p.window > 0 && ok) {
+      int seen = 0;
+      for (int i = 0; i < p.words && 64 * i < s.n; ++i) seen += __builtin_popcountll(r.mask[i] & kv_bits(0, s.n - 64 * i));
+      r.lo = max(base - max(p.window - seen, 0), 0);
+    }
+    r.hi = ok ? max(base, 0) : 0;
+  } else {
+    const KvRowRange x = kv_row_range(p, s, token);
+    r.mask = nullptr;
+    r.lo = x.lo;
+    r.hi = ok ? x.hi : 0;
+  }
+  r.sinks = min(p.sinks, r.hi);
+  return r;
+}
+// A row's bits of the page that begins at token j0 and holds `left` tokens.
+// (Pages that need them are few: what the row sees is found anew for each, so
+// that nothing of it is held all along the page loop.)
+__device__ __forceinline__ uint64_t kv_row_bits(const KvAttnMore& p, const KvSeq& s, const KvRowMore r, int j0, int left) {
+  uint64_t bits = kv_bits(r.lo - j0, r.hi - j0) | kv_bits(0, r.sinks - j0);
+  const int off = j0 - (s.len - s.n);  // of the page's first token in the tree
+  if (r.mask && off > -64 && off < s.n) {
+    uint64_t tree;
+    if (off < 0) {
+      tree = r.mask[0] << -off;
+    } else {
+      const int word = off >> 6, shift = off & 63;
+      tree = word < p.words ? r.mask[word] >> shift : 0ull;
+      if (shift > 0 && word + 1 < p.words) tree |= r.mask[word + 1] << (64 - shift);
+    }
+    bits |= tree & kv_bits(-off, s.n - off);
+  }
+  return bits & kv_bits(0, left);
+}
+__device__ __forceinline__ uint64_t kv_row_bits(const KvAttnMore& p, const KvSeq& s, int row, int rows, int j0, int left) {
+  asm volatile("" : "+v"(row));  // stays where it is called
+  const bool ok = row < rows;
+  return kv_row_bits(p, s, kv_row_more(p, s, ok ? row / p.group : 0, ok), j0, left);
+}
+
 // Floats of a part's result: (max, sum) of each row, then O [ROWS][D].
 __host__ __device__ constexpr int kv_part_floats(int rows, int D) { return rows * (D + 2); }
 
@@ -279,10 +386,11 @@ __device__ __forceinline__ kv_rsrc_t kv_rsrc(const void* base, int bytes) {
 struct KvPages {
   int ids;
   // page id of entry k (asked for in order); -1 past `end` or where the table holds no page
-  __device__ __forceinline__ int at(const KvAttnParams& p, int b, int first, int step, int end, int k) {
+  template <typename Real>
+  __device__ __forceinline__ int at(const KvAttnParams& p, int b, int first, int step, int end, int k, Real real) {
     if ((k & 63) == 0) {
       const int place = first + step * (k + ((int)threadIdx.x & 63));
-      ids = place < end ? kv_page(p.batch, b, place) : -1;
+      ids = place < end ? kv_page(p.batch, b, real(place)) : -1;
     }
     return __builtin_amdgcn_readlane(ids, k & 63);
   }
@@ -341,8 +449,9 @@ constexpr int kv_waves(int D) { return D <= 128 ? 8 : 4; }
 // table, two pages a wave and the join); one row each of 16 sequences of 1000
 // to 16000 tokens 41 us; five rows each of 32 sequences of 1024 to 16384
 // tokens (e4m3) 88 us (4.3 TB/s).
-template <int D, int FMT, int RT>
-__global__ __launch_bounds__(64 * kv_waves(D)) void kv_attn_rows_kernel(KvAttnParams p) {
+template <int D, int FMT, int RT, typename P>
+__global__ __launch_bounds__(64 * kv_waves(D)) void kv_attn_rows_kernel(P p) {
+  constexpr bool MORE = std::is_same_v<P, KvAttnMore>;
   constexpr int C = D / 64, N = D / 16, ROWS = 16 * RT, NW = kv_waves(D), THREADS = 64 * NW;
   constexpr bool BYTES = FMT == BQ_KV_I8;
   constexpr int JOIN = NW * (N * 256 + 32);
@@ -358,8 +467,16 @@ __global__ __launch_bounds__(64 * kv_waves(D)) void kv_attn_rows_kernel(KvAttnPa
 
   // the tile's pages, and the tokens that all its rows see
   const int tok0 = row0 / p.group, tok1 = min((row0 + ROWS - 1) / p.group, s.n - 1);
-  const KvRowRange r0 = kv_row_range(p, s, tok0), r1 = kv_row_range(p, s, tok1);
-  const int pa = r0.lo / kKvPage, pages = max((r1.hi + kKvPage - 1) / kKvPage - pa, 0);
+  const KvRowRange r0 = kv_first_range(p, s, tok0), r1 = kv_last_range(p, s, tok1);
+  const auto real = [&] {
+    if constexpr (MORE) return kv_places(p, r0, r1);
+    else return [](int at) { return at; };
+  }();
+  int pa = r0.lo / kKvPage, pages = max((r1.hi + kKvPage - 1) / kKvPage - pa, 0);
+  if constexpr (MORE) {
+    pages = max((r1.hi + kKvPage - 1) / kKvPage - real.gap, 0);
+    pa = 0;
+  }
   const int begin = pa + (w.parts > 1 ? w.split * w.chunk : 0);
   const int end = pa + (w.split == w.parts - 1 ? pages : min((w.split + 1) * w.chunk, pages));
 
@@ -367,7 +484,7 @@ __global__ __launch_bounds__(64 * kv_waves(D)) void kv_attn_rows_kernel(KvAttnPa
   // entry of one of 64 of them, so that no request waits for the table.
   KvPages pages_of;
   const auto place = [&](int k) -> int64_t {
-    const int page = pages_of.at(p, w.b, begin + wave, NW, end, k);
+    const int page = pages_of.at(p, w.b, begin + wave, NW, end, k, real);
     return page < 0 ? -1 : (int64_t)page * p.kv_heads + head;
   };
   const float scale = p.scale * kKvUnit<BYTES>;
@@ -401,9 +518,14 @@ __global__ __launch_bounds__(64 * kv_waves(D)) void kv_attn_rows_kernel(KvAttnPa
     const int row = row0 + 16 * t + r;
     const bool ok = row < rows;
     const int token = ok ? row / p.group : 0, qh = head * p.group + (ok ? row - token * p.group : 0);
-    const KvRowRange range = kv_row_range(p, s, token);
-    lo[t] = range.lo;
-    hi[t] = ok ? range.hi : 0;
+    if constexpr (MORE) {
+      lo[t] = 0;
+      hi[t] = ok ? r1.hi : 0;  // (above 0: a row)
+    } else {
+      const KvRowRange range = kv_row_range(p, s, token);
+      lo[t] = range.lo;
+      hi[t] = ok ? range.hi : 0;
+    }
     const _Float16* src = p.q + (int64_t)(s.q0 + token) * p.q_stride + qh * D + 16 * g;
 #pragma unroll
     for (int c = 0; c < 2 * C; ++c)
@@ -430,7 +552,7 @@ __global__ __launch_bounds__(64 * kv_waves(D)) void kv_attn_rows_kernel(KvAttnPa
 
   for (int at = begin + wave, k = 1; at < end; at += NW, ++k) {
     const int64_t next = place(k);
-    const int j0 = at * kKvPage;
+    const int j0 = real(at) * kKvPage;
     const int left = here < 0 ? 0 : s.len - j0;  // tokens of the page that are held
 
     // scores, in units of log2
@@ -458,20 +580,32 @@ __global__ __launch_bounds__(64 * kv_waves(D)) void kv_attn_rows_kernel(KvAttnPa
         for (int e = 0; e < 4; ++e) y[t][i][e] = BYTES ? __builtin_fmaf(y[t][i][e], c, off) : y[t][i][e] * c;
       }
     load_k(next);
-    if (left < kKvPage || j0 + kKvPage > r0.hi || j0 < r1.lo) {
+    if (left < kKvPage || ((j0 + kKvPage > r0.hi || j0 < r1.lo) && (!MORE || j0 + kKvPage > kv_sinks(p, r0.hi)))) {
       // a page that some row does not see whole: the row's tokens [lo, hi)
-      // as one unsigned comparison of each token
+      // as one unsigned comparison of each token, or by its bits
+      if constexpr (MORE) {
 #pragma unroll
-      for (int t = 0; t < RT; ++t) {
-        const int from = max(lo[t] - j0, 0), count = max(min(hi[t] - j0, left) - from, 0);
-        int in = 4 * g - from;
-        // stays in this branch: computed ahead of it, it would cost every page
-        asm volatile("" : "+v"(in));
+        for (int t = 0; t < RT; ++t) {
+          const uint64_t bits = kv_row_bits(p, s, row0 + 16 * t + r, rows, j0, left) >> (4 * g);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            y[t][i][e] = (unsigned)(in + 16 * i + e) < (unsigned)count ? y[t][i][e] : -__builtin_inff();
+            for (int e = 0; e < 4; ++e)
+              y[t][i][e] = (bits >> (16 * i + e)) & 1 ? y[t][i][e] : -__builtin_inff();
+        }
+      } else {
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+          const int from = max(lo[t] - j0, 0), count = max(min(hi[t] - j0, left) - from, 0);
+          int in = 4 * g - from;
+          // stays in this branch: computed ahead of it, it would cost every page
+          asm volatile("" : "+v"(in));
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              y[t][i][e] = (unsigned)(in + 16 * i + e) < (unsigned)count ? y[t][i][e] : -__builtin_inff();
+        }
       }
       // what lies past the length is never used: neither a scale (any in R's
       // range stands for it) nor, in e4m3, a code that is no number

@@ -1,6 +1,7 @@
 // C entry points of the rotary positions and of the paged 8-bit cache's
 // writing and reading.  Declarations are in include/bq.h.
 #include <algorithm>
+#include <cmath>
 
 #include "kv_cache_kernels.hpp"
 
@@ -33,33 +34,24 @@ int rope_tokens_per_wg(int tokens, int rot_dim, int units, int threads) {
   return best;
 }
 
-}  // namespace
-
-extern "C" {
-
-int bq_rope(const void* x, void* y, long long x_stride, long long y_stride, int tokens, int heads, int head_dim,
-            const int* pos, const float* inv_freq, const int* axis, int rot_dim, int axes, int flags, void* stream) {
-  if (tokens > 0 && (!x || !y)) return BQ_ERR_NULL;
-  if (tokens < 0 || tokens > (1 << 28) || heads < 1 || heads > 65536 || head_dim < 16 || head_dim > 1024 ||
-      head_dim % 16 != 0)
-    return BQ_ERR_SHAPE;
-  const int st = check_angles(pos, inv_freq, axis, rot_dim, axes, flags, head_dim, tokens);
-  if (st != BQ_OK) return st;
-  if (!kv_rows_ok(x, x_stride, heads * head_dim) || !kv_rows_ok(y, y_stride, heads * head_dim)) return BQ_ERR_ALIGN;
-  if (tokens == 0) return BQ_OK;
-  RopeParams p{};
-  p.rows = RopeRows{static_cast<const _Float16*>(x), static_cast<_Float16*>(y), x_stride, y_stride, heads, head_dim};
-  p.a = angles(pos, inv_freq, axis, rot_dim, axes, flags, tokens);
-  p.tokens_per_wg = rope_tokens_per_wg(tokens, rot_dim, heads * head_dim / 16, 256);
-  return kv_launch(reinterpret_cast<const void*>(&rope_kernel),
-                   dim3((unsigned)((tokens + p.tokens_per_wg - 1) / p.tokens_per_wg)), dim3(256), 0, stream, &p);
+// Arguments of a norm: w null is none.
+int check_norm(const float* w, float eps) {
+  if (!kv_aligned(w, 4)) return BQ_ERR_ALIGN;
+  return std::isfinite(eps) && eps >= 0.f ? BQ_OK : BQ_ERR_SHAPE;
 }
 
-int bq_kv_append(const bq_kv_cache* cache, int layer, const void* k, const void* v, long long k_stride,
-                 long long v_stride, const void* q, void* q_out, long long q_stride, long long q_out_stride,
-                 int q_heads, const int* cu, const int* lens, const int* table, int batch, int max_pages, int total,
-                 const int* pos, const float* inv_freq, const int* axis, int rot_dim, int axes, int flags,
-                 void* stream) {
+template <bool NORM>
+const void* pick_append(int per) {
+  return per == 4 ? reinterpret_cast<const void*>(&kv_append_kernel<4, NORM>)
+       : per == 2 ? reinterpret_cast<const void*>(&kv_append_kernel<2, NORM>)
+                  : reinterpret_cast<const void*>(&kv_append_kernel<1, NORM>);
+}
+
+int append(const bq_kv_cache* cache, int layer, const void* k, const void* v, long long k_stride,
+           long long v_stride, const void* q, void* q_out, long long q_stride, long long q_out_stride,
+           int q_heads, const int* cu, const int* lens, const int* table, int batch, int max_pages, int total,
+           const int* pos, const float* inv_freq, const int* axis, int rot_dim, int axes, int flags,
+           const NormWeight& k_norm, const NormWeight& q_norm, void* stream) {
   int st = kv_check_cache(cache);
   if (st != BQ_OK) return st;
   if (total > 0 && (!k || !v || (q && !q_out))) return BQ_ERR_NULL;
@@ -73,7 +65,7 @@ int bq_kv_append(const bq_kv_cache* cache, int layer, const void* k, const void*
   if (!kv_rows_ok(k, k_stride, cache->kv_heads * D) || !kv_rows_ok(v, v_stride, cache->kv_heads * D)) return BQ_ERR_ALIGN;
   if (q && (!kv_rows_ok(q, q_stride, q_heads * D) || !kv_rows_ok(q_out, q_out_stride, q_heads * D))) return BQ_ERR_ALIGN;
   if (total == 0) return BQ_OK;
-  KvAppendParams p{};
+  KvAppendNormParams p{};
   const size_t at = (size_t)layer * kv_layer_heads(cache);
   p.k = static_cast<uint8_t*>(cache->k) + at * kv_head_bytes(cache);
   p.v = static_cast<uint8_t*>(cache->v) + at * kv_head_bytes(cache);
@@ -98,14 +90,82 @@ int bq_kv_append(const bq_kv_cache* cache, int layer, const void* k, const void*
   // with two and 20.6 with four, eight times 301 tokens 31.6 and 27.0.
   const int per = total < 16 * (int64_t)batch || items > 128 ? 4 : D <= 128 ? 1 : 2;
   const int threads = 2 * D * (kKvBlocks / per);
-  p.q_tokens_per_wg = rope_tokens_per_wg(total, rot_dim, q_heads * D / 16, threads);
+  const bool norm = k_norm.w || q_norm.w;
+  p.k_norm = k_norm;
+  p.q_norm = q_norm;
+  p.q_tokens_per_wg = rope_tokens_per_wg(total, rot_dim, q_heads * (q_norm.w ? norm_lanes(D) : D / 16), threads);
   const int64_t q_wgs = q ? (total + p.q_tokens_per_wg - 1) / p.q_tokens_per_wg : 0;
   if (items + q_wgs > 0x7FFFFFFF) return BQ_ERR_SHAPE;
   p.items = (int)items;
-  const void* fn = per == 4 ? reinterpret_cast<const void*>(&kv_append_kernel<4>)
-                 : per == 2 ? reinterpret_cast<const void*>(&kv_append_kernel<2>)
-                            : reinterpret_cast<const void*>(&kv_append_kernel<1>);
+  const void* fn = norm ? pick_append<true>(per) : pick_append<false>(per);
   return kv_launch(fn, dim3((unsigned)(items + q_wgs)), dim3((unsigned)threads), 0, stream, &p);
+}
+
+}  // namespace
+
+extern "C" {
+
+int bq_rope(const void* x, void* y, long long x_stride, long long y_stride, int tokens, int heads, int head_dim,
+            const int* pos, const float* inv_freq, const int* axis, int rot_dim, int axes, int flags, void* stream) {
+  if (tokens > 0 && (!x || !y)) return BQ_ERR_NULL;
+  if (tokens < 0 || tokens > (1 << 28) || heads < 1 || heads > 65536 || head_dim < 16 || head_dim > 1024 ||
+      head_dim % 16 != 0)
+    return BQ_ERR_SHAPE;
+  const int st = check_angles(pos, inv_freq, axis, rot_dim, axes, flags, head_dim, tokens);
+  if (st != BQ_OK) return st;
+  if (!kv_rows_ok(x, x_stride, heads * head_dim) || !kv_rows_ok(y, y_stride, heads * head_dim)) return BQ_ERR_ALIGN;
+  if (tokens == 0) return BQ_OK;
+  RopeParams p{};
+  p.rows = RopeRows{static_cast<const _Float16*>(x), static_cast<_Float16*>(y), x_stride, y_stride, heads, head_dim};
+  p.a = angles(pos, inv_freq, axis, rot_dim, axes, flags, tokens);
+  p.tokens_per_wg = rope_tokens_per_wg(tokens, rot_dim, heads * head_dim / 16, 256);
+  return kv_launch(reinterpret_cast<const void*>(&rope_kernel),
+                   dim3((unsigned)((tokens + p.tokens_per_wg - 1) / p.tokens_per_wg)), dim3(256), 0, stream, &p);
+}
+
+int bq_norm_rope(const void* x, void* y, long long x_stride, long long y_stride, int tokens, int heads, int head_dim,
+                 const float* weight, float eps, const int* pos, const float* inv_freq, const int* axis, int rot_dim,
+                 int axes, int flags, void* stream) {
+  if (tokens > 0 && (!x || !y)) return BQ_ERR_NULL;
+  if (!weight) return BQ_ERR_NULL;
+  if (tokens < 0 || tokens > (1 << 28) || heads < 1 || heads > 65536 || head_dim < 16 || head_dim > 1024 ||
+      head_dim % 16 != 0)
+    return BQ_ERR_SHAPE;
+  int st = check_norm(weight, eps);
+  if (st != BQ_OK) return st;
+  st = check_angles(pos, inv_freq, axis, rot_dim, axes, flags, head_dim, tokens);
+  if (st != BQ_OK) return st;
+  if (!kv_rows_ok(x, x_stride, heads * head_dim) || !kv_rows_ok(y, y_stride, heads * head_dim)) return BQ_ERR_ALIGN;
+  if (tokens == 0) return BQ_OK;
+  NormRopeParams p{};
+  p.rows = RopeRows{static_cast<const _Float16*>(x), static_cast<_Float16*>(y), x_stride, y_stride, heads, head_dim};
+  p.a = angles(pos, inv_freq, axis, rot_dim, axes, flags, tokens);
+  p.norm = NormWeight{weight, eps};
+  p.tokens_per_wg = rope_tokens_per_wg(tokens, rot_dim, heads * norm_lanes(head_dim), 256);
+  return kv_launch(reinterpret_cast<const void*>(&norm_rope_kernel),
+                   dim3((unsigned)((tokens + p.tokens_per_wg - 1) / p.tokens_per_wg)), dim3(256), 0, stream, &p);
+}
+
+int bq_kv_append(const bq_kv_cache* cache, int layer, const void* k, const void* v, long long k_stride,
+                 long long v_stride, const void* q, void* q_out, long long q_stride, long long q_out_stride,
+                 int q_heads, const int* cu, const int* lens, const int* table, int batch, int max_pages, int total,
+                 const int* pos, const float* inv_freq, const int* axis, int rot_dim, int axes, int flags,
+                 void* stream) {
+  return append(cache, layer, k, v, k_stride, v_stride, q, q_out, q_stride, q_out_stride, q_heads, cu, lens, table,
+                batch, max_pages, total, pos, inv_freq, axis, rot_dim, axes, flags, NormWeight{}, NormWeight{}, stream);
+}
+
+int bq_kv_append_norm(const bq_kv_cache* cache, int layer, const void* k, const void* v, long long k_stride,
+                      long long v_stride, const void* q, void* q_out, long long q_stride, long long q_out_stride,
+                      int q_heads, const int* cu, const int* lens, const int* table, int batch, int max_pages,
+                      int total, const float* k_weight, const float* q_weight, float eps, const int* pos,
+                      const float* inv_freq, const int* axis, int rot_dim, int axes, int flags, void* stream) {
+  int st = check_norm(k_weight, eps);
+  if (st == BQ_OK) st = check_norm(q_weight, eps);
+  if (st != BQ_OK) return st;
+  return append(cache, layer, k, v, k_stride, v_stride, q, q_out, q_stride, q_out_stride, q_heads, cu, lens, table,
+                batch, max_pages, total, pos, inv_freq, axis, rot_dim, axes, flags, NormWeight{k_weight, eps},
+                NormWeight{q ? q_weight : nullptr, eps}, stream);
 }
 
 int bq_kv_read(const bq_kv_cache* cache, int layer, void* k, void* v, const int* cu, const int* lens, const int* table,

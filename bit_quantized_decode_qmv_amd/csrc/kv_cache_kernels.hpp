@@ -16,7 +16,12 @@
 // codes each new value as rne(x / s), brings the codes of older tokens of
 // the block to the new scale (unchanged when the scale did not grow), and
 // clears the block's tokens past len.
+//
+// Norms: where a row is normed first, x is x * rsqrt(mean(x^2) + eps) * w over
+// its head's dimensions, in fp32 and without a rounding of its own.
 #pragma once
+
+#include <type_traits>
 
 #include "kv_common.hpp"
 
@@ -153,6 +158,101 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeParams p) {
   rope_rows(p.rows, p.a, t0, min(p.tokens_per_wg, p.a.total - t0), (int)threadIdx.x, 256, table);
 }
 
+// A norm of each head's row ahead of the rotation.
+struct NormWeight {
+  const float* w;  // [head_dim], or null: no norm
+  float eps;
+};
+// Lanes that a head's row takes where it is normed: its units, filled up to a
+// power of two, so that a row's sum stays inside a wave.
+__host__ __device__ inline int norm_lanes(int head_dim) {
+  int lanes = 1;
+  while (lanes * 16 < head_dim) lanes *= 2;
+  return lanes;
+}
+
+// rope_rows with a norm: a thread's unit is the same in all of its rounds
+// (a round is a multiple of 64 threads), so its sixteen weights stay in
+// registers, and a row's sum of squares is the work of `lanes` lanes side by
+// side.  Bound by HBM like the rotation alone; the sum is hidden behind the
+// loads of the other rounds.
+__device__ __forceinline__ void norm_rope_rows(const RopeRows& p, const RopeAngles& a, const NormWeight& norm, int token0,
+                                               int tokens, int thread, int threads, float2* table) {
+  const int half = a.rot >> 1;
+  for (int i = thread; i < tokens * half; i += threads) {
+    const int t = (int)((unsigned)i / (unsigned)half);
+    table[i] = rope_pair(a, i - t * half, token0 + t);
+  }
+  const int lanes = norm_lanes(p.head_dim), per = p.heads * lanes, all = tokens * per;
+  const int unit = thread & (lanes - 1);
+  const bool mine = unit < (p.head_dim >> 4), turns = unit < (a.rot >> 4);
+  int lo, hi;
+  rope_unit_at(a, mine ? unit : 0, lo, hi);
+  float w[16];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    w[j] = norm.w[lo + j];
+    w[8 + j] = norm.w[hi + j];
+  }
+  const float mean = 1.f / (float)p.head_dim;
+  __syncthreads();
+  constexpr int AT_ONCE = kRopeAtOnce;
+  for (int i0 = thread; i0 < all; i0 += AT_ONCE * threads) {
+    half8_t v[AT_ONCE][2];
+    int tok[AT_ONCE], at[AT_ONCE];
+#pragma unroll
+    for (int k = 0; k < AT_ONCE; ++k) {
+      const int i = min(i0 + k * threads, all - 1);  // no branch: the last row is read again
+      tok[k] = (int)((unsigned)i / (unsigned)per);
+      at[k] = (int)((unsigned)(i - tok[k] * per) / (unsigned)lanes) * p.head_dim;
+      const _Float16* x = p.x + (int64_t)(token0 + tok[k]) * p.x_stride + at[k];
+      v[k][0] = *reinterpret_cast<const half8_t*>(x + lo);
+      v[k][1] = *reinterpret_cast<const half8_t*>(x + hi);
+    }
+#pragma unroll
+    for (int k = 0; k < AT_ONCE; ++k) {
+      float y[16], sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        y[j] = (float)v[k][0][j];
+        y[8 + j] = (float)v[k][1][j];
+      }
+#pragma unroll
+      for (int j = 0; j < 16; ++j) sum = __builtin_fmaf(y[j], y[j], sum);
+      sum = mine ? sum : 0.f;
+      for (int o = lanes >> 1; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
+      const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(sum, mean, norm.eps));
+      if (!mine || i0 + k * threads >= all) continue;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) y[j] *= r * w[j];
+      if (turns) {
+        float2 cs[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) cs[j] = table[tok[k] * half + unit * 8 + j];
+        rope_turn(a.adjacent, cs, y);
+      }
+      half8_t o[2];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        o[0][j] = (_Float16)y[j];
+        o[1][j] = (_Float16)y[8 + j];
+      }
+      _Float16* to = p.y + (int64_t)(token0 + tok[k]) * p.y_stride + at[k];
+      *reinterpret_cast<half8_t*>(to + lo) = o[0];
+      *reinterpret_cast<half8_t*>(to + hi) = o[1];
+    }
+  }
+}
+
+struct NormRopeParams : RopeParams {
+  NormWeight norm;
+};
+__global__ __launch_bounds__(256) void norm_rope_kernel(NormRopeParams p) {
+  __shared__ float2 table[kRopeTable];
+  const int t0 = (int)blockIdx.x * p.tokens_per_wg;
+  norm_rope_rows(p.rows, p.a, p.norm, t0, min(p.tokens_per_wg, p.a.total - t0), (int)threadIdx.x, 256, table);
+}
+
 struct KvAppendParams {
   uint8_t *k, *v;               // the layer's codes
   float *ks, *vs;               // and scales
@@ -163,6 +263,9 @@ struct KvAppendParams {
   KvBatch batch;
   int kv_heads, head_dim, format;
   int items, q_tokens_per_wg;   // page items (at most), then workgroups over q
+};
+struct KvAppendNormParams : KvAppendParams {
+  NormWeight k_norm, q_norm;
 };
 
 // Four dwords of four bytes each, transposed.
@@ -184,8 +287,12 @@ __device__ __forceinline__ void kv_transpose4(const uint32_t (&x)[4], uint32_t (
 // Long calls are bound by HBM, short ones by the chain of latencies from the
 // table to the page.  Measured, 8 heads of 128 and q of 48: 4093 tokens 30 us
 // (4.2 TB/s), one token each of 32 sequences 7.7 us.
-template <int PER>
-__global__ __launch_bounds__(PER == 4 ? 512 : 1024) void kv_append_kernel(KvAppendParams p) {
+// NORM: a token's units lie on D / 16 threads side by side, of two waves where
+// D is 192; their sums of squares are exchanged through LDS ahead of the
+// barrier that the angles' table needs anyway.
+template <int PER, bool NORM = false>
+__global__ __launch_bounds__(PER == 4 ? 512 : 1024) void kv_append_kernel(
+    std::conditional_t<NORM, KvAppendNormParams, KvAppendParams> p) {
   __shared__ float red[2][kKvBlocks][4];
   __shared__ __align__(16) uint8_t codes[2][kKvPage * 256];
   __shared__ RopeFreq freq[128];
@@ -193,6 +300,13 @@ __global__ __launch_bounds__(PER == 4 ? 512 : 1024) void kv_append_kernel(KvAppe
   const int D = p.head_dim, units = D >> 4;
   if ((int)blockIdx.x >= p.items) {
     const int t0 = ((int)blockIdx.x - p.items) * p.q_tokens_per_wg;
+    if constexpr (NORM) {
+      if (p.q_norm.w) {
+        norm_rope_rows(p.q, p.a, p.q_norm, t0, min(p.q_tokens_per_wg, p.batch.total - t0), (int)threadIdx.x,
+                       (int)blockDim.x, reinterpret_cast<float2*>(codes));
+        return;
+      }
+    }
     rope_rows(p.q, p.a, t0, min(p.q_tokens_per_wg, p.batch.total - t0), (int)threadIdx.x, (int)blockDim.x,
               reinterpret_cast<float2*>(codes));
     return;
@@ -253,6 +367,32 @@ __global__ __launch_bounds__(PER == 4 ? 512 : 1024) void kv_append_kernel(KvAppe
     }
   }
   const bool turns = !which && unit < (p.a.rot >> 4);
+  [[maybe_unused]] float w[16];
+  [[maybe_unused]] float(*squares)[kKvBlock][17] = nullptr;  // [block][token][unit], in LDS that the codes take later
+  [[maybe_unused]] bool norms = false;
+  if constexpr (NORM) {
+    norms = !which && p.k_norm.w;
+    squares = reinterpret_cast<float(*)[kKvBlock][17]>(&codes[1][0]);
+    if (norms) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        w[j] = p.k_norm.w[lo + j];
+        w[8 + j] = p.k_norm.w[hi + j];
+      }
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int t = t00 + (i0 + i) * kKvBlock + tok;
+        if (t < start || t >= s.len) continue;
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float a = (float)raw[i][0][j], b = (float)raw[i][1][j];
+          sum = __builtin_fmaf(a, a, __builtin_fmaf(b, b, sum));
+        }
+        squares[i0 + i][tok][unit] = sum;
+      }
+    }
+  }
   if (p.a.rot > 0) {
     for (int i = (int)threadIdx.x; i < (p.a.rot >> 1); i += (int)blockDim.x) {
       freq[i] = rope_freq(p.a.inv_freq[i]);
@@ -275,6 +415,15 @@ __global__ __launch_bounds__(PER == 4 ? 512 : 1024) void kv_append_kernel(KvAppe
       for (int j = 0; j < 8; ++j) {
         x[i][j] = (float)raw[i][0][j];
         x[i][8 + j] = (float)raw[i][1][j];
+      }
+      if constexpr (NORM) {
+        if (norms) {
+          float sum = 0.f;
+          for (int u = 0; u < units; ++u) sum += squares[i0 + i][tok][u];
+          const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(sum, 1.f / (float)D, p.k_norm.eps));
+#pragma unroll
+          for (int j = 0; j < 16; ++j) x[i][j] *= r * w[j];
+        }
       }
       if (turns) {
         float2 cs[8];

@@ -63,8 +63,9 @@ __device__ __forceinline__ void kv_stay(f32x4& x) {
 constexpr int kPromptWaves = 4, kPromptThreads = 64 * kPromptWaves;
 constexpr int kPromptRows = 32 * kPromptWaves;
 
-template <int D, int FMT>
-__global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prompt_kernel(KvAttnParams p) {
+template <int D, int FMT, typename P>
+__global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prompt_kernel(P p) {
+  constexpr bool MORE = std::is_same_v<P, KvAttnMore>;
   constexpr int C = D / 64, N = D / 16, UNITS = 4 * D / kPromptThreads;  // 16-byte units of K (or V) a thread
   constexpr bool BYTES = FMT == BQ_KV_I8;
   // [buffer][K, V][operand][lane][8]
@@ -78,14 +79,22 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
   const KvSeq s = w.s;
   const int rows = s.n * p.group;
   const int row0 = w.tile * kPromptRows, row1 = min(row0 + kPromptRows, rows) - 1;
-  const KvRowRange r0 = kv_row_range(p, s, row0 / p.group), r1 = kv_row_range(p, s, row1 / p.group);
-  const int pa = r0.lo / kKvPage, pages = max((r1.hi + kKvPage - 1) / kKvPage - pa, 0);
+  const KvRowRange r0 = kv_first_range(p, s, row0 / p.group), r1 = kv_last_range(p, s, row1 / p.group);
+  const auto real = [&] {
+    if constexpr (MORE) return kv_places(p, r0, r1);
+    else return [](int at) { return at; };
+  }();
+  int pa = r0.lo / kKvPage, pages = max((r1.hi + kKvPage - 1) / kKvPage - pa, 0);
+  if constexpr (MORE) {
+    pages = max((r1.hi + kKvPage - 1) / kKvPage - real.gap, 0);
+    pa = 0;
+  }
   const int begin = pa + (w.parts > 1 ? w.split * w.chunk : 0);
   const int end = pa + (w.split == w.parts - 1 ? pages : min((w.split + 1) * w.chunk, pages));
 
   KvPages pages_of;
   const auto place = [&](int k) -> int64_t {
-    const int page = pages_of.at(p, w.b, begin, 1, end, k);
+    const int page = pages_of.at(p, w.b, begin, 1, end, k, real);
     return page < 0 ? -1 : (int64_t)page * p.kv_heads + head;
   };
   // a page's scales are requested ahead of its codes: what waits for them
@@ -134,7 +143,7 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
   {
     const int first = row0 + 32 * wave, last = min(first + 31, rows - 1);
     if (first < rows) {
-      const KvRowRange a = kv_row_range(p, s, first / p.group), b = kv_row_range(p, s, last / p.group);
+      const KvRowRange a = kv_first_range(p, s, first / p.group), b = kv_last_range(p, s, last / p.group);
       wave_lo = a.lo;
       wave_hi = b.hi;
       all_lo = b.lo;
@@ -146,9 +155,14 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
     const int row = row0 + 32 * wave + 16 * t + r;
     const bool ok = row < rows;
     const int token = ok ? row / p.group : 0, qh = head * p.group + (ok ? row - token * p.group : 0);
-    const KvRowRange range = kv_row_range(p, s, token);
-    lo[t] = range.lo;
-    hi[t] = ok ? range.hi : 0;
+    if constexpr (MORE) {
+      lo[t] = 0;
+      hi[t] = ok ? wave_hi : 0;  // (above 0: a row)
+    } else {
+      const KvRowRange range = kv_row_range(p, s, token);
+      lo[t] = range.lo;
+      hi[t] = ok ? range.hi : 0;
+    }
     const _Float16* src = p.q + (int64_t)(s.q0 + token) * p.q_stride + qh * D + 16 * g;
 #pragma unroll
     for (int c = 0; c < 2 * C; ++c) {
@@ -184,7 +198,7 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
     for (int n = 0; n < N; ++n) o[t][n] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
 
-  stage(0, here < 0 ? 0 : s.len - begin * kKvPage);
+  stage(0, here < 0 ? 0 : s.len - real(begin) * kKvPage);
   __syncthreads();
   for (int at = begin; at < end; ++at) {
     const int buf = (at - begin) & 1;
@@ -196,9 +210,9 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
     const f32x4 sk = sk_next;
     f32x4 sv = sv_next;
     request(next);
-    const int j0 = at * kKvPage, left = here < 0 ? 0 : s.len - j0;
+    const int j0 = real(at) * kKvPage, left = here < 0 ? 0 : s.len - j0;
 
-    if (j0 < wave_hi && j0 + kKvPage > wave_lo) {
+    if ((j0 < wave_hi && j0 + kKvPage > wave_lo) || (MORE && j0 < kv_sinks(p, wave_hi))) {
       f32x4 y[2][4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -215,7 +229,7 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
 #pragma unroll
       for (int i = 0; i < 4; ++i) kv_stay<D, false>(y[0][i]), kv_stay<D, false>(y[1][i]);
       f32x4 c = sk * scale;
-      if (left < kKvPage || j0 + kKvPage > all_hi || j0 < all_lo) {
+      if (left < kKvPage || ((j0 + kKvPage > all_hi || j0 < all_lo) && (!MORE || j0 + kKvPage > kv_sinks(p, all_hi)))) {
         // a page that some row does not see whole; a block past the length
         // has no scale (its probabilities are 0 under any)
         int held = left;
@@ -228,16 +242,28 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
               sv[i] = held > 0 ? sv[0] : kv_exp_float(unit_ex);
             }
         }
+        if constexpr (MORE) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int from = max(lo[t] - j0, 0), count = max(min(hi[t] - j0, left) - from, 0);
-          int in = 4 * g - from;
-          asm volatile("" : "+v"(in));
+          for (int t = 0; t < 2; ++t) {
+            const uint64_t bits = kv_row_bits(p, s, row0 + 32 * wave + 16 * t + r, rows, j0, left) >> (4 * g);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              y[t][i][e] = (unsigned)(in + 16 * i + e) < (unsigned)count ? y[t][i][e] * c[i] : -__builtin_inff();
+              for (int e = 0; e < 4; ++e)
+                y[t][i][e] = (bits >> (16 * i + e)) & 1 ? y[t][i][e] * c[i] : -__builtin_inff();
+          }
+        } else {
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const int from = max(lo[t] - j0, 0), count = max(min(hi[t] - j0, left) - from, 0);
+            int in = 4 * g - from;
+            asm volatile("" : "+v"(in));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                y[t][i][e] = (unsigned)(in + 16 * i + e) < (unsigned)count ? y[t][i][e] * c[i] : -__builtin_inff();
+          }
         }
         c = f32x4{1.f, 1.f, 1.f, 1.f};  // a hidden score times 0 would be no number
       }
@@ -367,7 +393,7 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
         }
       kv_order_reads<2 * N, 4>();
     }
-    stage(buf ^ 1, next < 0 ? 0 : s.len - j0 - kKvPage);
+    stage(buf ^ 1, next < 0 ? 0 : s.len - (MORE ? real(at + 1) * kKvPage : j0 + kKvPage));
     here = next;
     __syncthreads();
   }
@@ -400,8 +426,8 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
 
 // Joins the parts of the tiles that have several, in order; a workgroup takes
 // 16 rows of a tile.
-template <int D>
-__global__ __launch_bounds__(256) void kv_attn_join_kernel(KvAttnParams p) {
+template <int D, typename P>
+__global__ __launch_bounds__(256) void kv_attn_join_kernel(P p) {
   constexpr int SLOT = kv_part_floats(kPromptRows, D);
   __shared__ float f[kKvMaxParts][16];
   const int head = (int)blockIdx.x, item = (int)blockIdx.y / (kPromptRows / 16), first = (int)blockIdx.y % (kPromptRows / 16) * 16;

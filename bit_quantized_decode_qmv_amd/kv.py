@@ -1,7 +1,9 @@
 """Attention with a paged key/value cache in 8 bits: the binding of the
-``bq_rope`` and ``bq_kv_*`` entry points of ``include/bq.h`` and their tensor
-helpers (``rope``, ``kv_append``, ``kv_read``, ``kv_attn``, ``kv_fork``,
-``kv_resize``, ``kv_compact``, ``kv_copy_pages``) over a :class:`KVCache`.
+``bq_rope``, ``bq_norm_rope`` and ``bq_kv_*`` entry points of ``include/bq.h``
+and their tensor helpers (``rope``, ``norm_rope``, ``kv_append``,
+``kv_append_norm``, ``kv_read``, ``kv_attn``, ``kv_attn_tree``, ``kv_keep``,
+``kv_fork``, ``kv_resize``, ``kv_compact``, ``kv_copy_pages``) over a
+:class:`KVCache`.
 
 As in the rest of the package every step runs in the HIP kernels; a helper
 checks its arguments, allocates what it returns and passes the current stream.
@@ -21,9 +23,12 @@ KV_CAUSAL = 1
 KV_ATTN_COUNTER_BYTES = 65536
 ROPE_ADJACENT = 1
 ROPE_MAX_AXES = 8
+TREE_MAX_WORDS = 16
+TREE_MAX_ROWS = 1024
 
 KV_POINTS = ("bq_rope", "bq_kv_append", "bq_kv_read", "bq_kv_attn_workspace", "bq_kv_attn", "bq_kv_pages_workspace",
-             "bq_kv_fork", "bq_kv_resize", "bq_kv_compact", "bq_kv_copy_pages")
+             "bq_kv_fork", "bq_kv_resize", "bq_kv_compact", "bq_kv_copy_pages", "bq_norm_rope", "bq_kv_append_norm",
+             "bq_kv_attn_sinks", "bq_kv_attn_tree", "bq_kv_keep")
 
 
 class KVCacheDesc(ctypes.Structure):
@@ -35,7 +40,7 @@ class KVCacheDesc(ctypes.Structure):
 
 def declare(lib) -> None:
     """Argument types of the entry points."""
-    vp, i, ll, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_size_t
+    vp, i, ll, sz, f = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_size_t, ctypes.c_float
     cache = ctypes.POINTER(KVCacheDesc)
     size = ctypes.POINTER(sz)
     types = {
@@ -49,6 +54,12 @@ def declare(lib) -> None:
         "bq_kv_resize": [cache, vp, vp, vp, i, i, vp, vp, vp, sz, vp],
         "bq_kv_compact": [cache, vp, vp, i, i, vp, vp, sz, vp],
         "bq_kv_copy_pages": [cache, vp, vp, i, vp],
+        "bq_norm_rope": [vp, vp, ll, ll, i, i, i, vp, f, vp, vp, vp, i, i, i, vp],
+        "bq_kv_append_norm": [cache, i, vp, vp, ll, ll, vp, vp, ll, ll, i, vp, vp, vp, i, i, i, vp, vp, f, vp, vp, vp, i, i,
+                              i, vp],
+        "bq_kv_attn_sinks": [cache, i, vp, vp, ll, ll, i, vp, vp, vp, i, i, i, f, i, i, vp, sz, vp],
+        "bq_kv_attn_tree": [cache, i, vp, vp, ll, ll, i, vp, vp, vp, i, i, i, vp, i, f, i, i, vp, sz, vp],
+        "bq_kv_keep": [cache, vp, vp, vp, i, i, vp, i, vp, vp],
     }
     for name, args in types.items():
         fn = getattr(lib, name)
@@ -124,6 +135,11 @@ bq_kv_fork = _c_entry("bq_kv_fork")
 bq_kv_resize = _c_entry("bq_kv_resize")
 bq_kv_compact = _c_entry("bq_kv_compact")
 bq_kv_copy_pages = _c_entry("bq_kv_copy_pages")
+bq_norm_rope = _c_entry("bq_norm_rope")
+bq_kv_append_norm = _c_entry("bq_kv_append_norm")
+bq_kv_attn_sinks = _c_entry("bq_kv_attn_sinks")
+bq_kv_attn_tree = _c_entry("bq_kv_attn_tree")
+bq_kv_keep = _c_entry("bq_kv_keep")
 
 
 def bq_kv_attn_workspace(desc, q_heads, batch, total):
@@ -285,12 +301,53 @@ def rope(x, pos, inv_freq, axis=None, adjacent: bool = False, out=None):
     return out
 
 
+def _weight(w, name, head_dim, device):
+    """Checks a norm's weights; their pointer, or None."""
+    if w is None:
+        return None
+    _need(w, name, _torch.float32, device)
+    if w.shape != (head_dim,):
+        raise ValueError(f"{name} has shape {tuple(w.shape)}, expected ({head_dim},)")
+    return w.data_ptr()
+
+
+def norm_rope(x, weight, eps: float, pos=None, inv_freq=None, axis=None, adjacent: bool = False, out=None):
+    """x [tokens][heads][head_dim], each head's row normed (x * weight /
+    sqrt(mean(x^2) + eps), weight float32 [head_dim]) and then turned as
+    rope() does, in one pass; without inv_freq nothing turns.  out may be x."""
+    stride = _rows(x, "x", None)
+    dev = x.device
+    tokens, heads, dim = x.shape
+    if weight is None:
+        raise TypeError("weight must be a torch.Tensor")
+    w = _weight(weight, "weight", dim, dev)
+    a = _angles(pos, inv_freq, axis, adjacent, tokens, dev)
+    out, out_stride = _out(out, "out", x, dev)
+    _launch(dev, "bq_norm_rope", x.data_ptr(), out.data_ptr(), stride, out_stride, tokens, heads, dim, w, eps, *a)
+    return out
+
+
 def kv_append(cache: KVCache, layer: int, k, v, cu, lens, table, q=None, pos=None, inv_freq=None, axis=None,
               adjacent: bool = False, q_out=None):
     """Writes the rows k, v [total][kv_heads][head_dim] to the cache as the
     last tokens of their sequences (lens counts them), k turned as rope()
     does; with q [total][q_heads][head_dim] also returns q turned (into q_out
     when given).  Without inv_freq nothing turns."""
+    return _append("bq_kv_append", cache, layer, k, v, cu, lens, table, q, pos, inv_freq, axis, adjacent, q_out)
+
+
+def kv_append_norm(cache: KVCache, layer: int, k, v, cu, lens, table, q=None, k_weight=None, q_weight=None,
+                   eps: float = 1e-6, pos=None, inv_freq=None, axis=None, adjacent: bool = False, q_out=None):
+    """kv_append() with each head's row of k normed by k_weight and of q by
+    q_weight ahead of the rotation, as norm_rope() does (float32 [head_dim];
+    None: not normed)."""
+    _torch or _use_torch()
+    norm = (_weight(k_weight, "k_weight", cache.head_dim, cache.device),
+            _weight(q_weight, "q_weight", cache.head_dim, cache.device), eps)
+    return _append("bq_kv_append_norm", cache, layer, k, v, cu, lens, table, q, pos, inv_freq, axis, adjacent, q_out, norm)
+
+
+def _append(name, cache, layer, k, v, cu, lens, table, q, pos, inv_freq, axis, adjacent, q_out, norm=()):
     dev = cache.device
     k_stride = _rows(k, "k", dev, cache.kv_heads, cache.head_dim)
     v_stride = _rows_like(v, "v", k, dev)
@@ -305,8 +362,9 @@ def kv_append(cache: KVCache, layer: int, k, v, cu, lens, table, q=None, pos=Non
             raise ValueError(f"q has {q.shape[0]} rows, k {total}")
         q_out, out_stride = _out(q_out, "q_out", q, dev)
         qp, op, q_heads = q.data_ptr(), q_out.data_ptr(), q.shape[1]
-    _launch(dev, "bq_kv_append", cache.desc, _int(layer, "layer"), k.data_ptr(), v.data_ptr(), k_stride, v_stride, qp, op,
-            q_stride, out_stride, q_heads, cu.data_ptr(), lens.data_ptr(), table.data_ptr(), batch, max_pages, total, *a)
+    _launch(dev, name, cache.desc, _int(layer, "layer"), k.data_ptr(), v.data_ptr(), k_stride, v_stride, qp, op,
+            q_stride, out_stride, q_heads, cu.data_ptr(), lens.data_ptr(), table.data_ptr(), batch, max_pages, total,
+            *norm, *a)
     return q_out if q is not None else None
 
 
@@ -323,13 +381,41 @@ def kv_read(cache: KVCache, layer: int, cu, lens, table, total: int):
 
 
 def kv_attn(cache: KVCache, layer: int, q, cu, lens, table, scale: Optional[float] = None, causal: bool = True,
-            window: int = 0, out=None, workspace=None):
+            window: int = 0, out=None, workspace=None, sinks: int = 0):
     """Attention of the rows q [total][q_heads][head_dim] over the cache; scale
     defaults to head_dim ** -0.5.  causal: a row sees the tokens up to its own
     position (the rows are the last of their sequence), window > 0: only the
-    last `window` of them; else every token held.  workspace: a uint8 tensor,
-    zero before its first use and kept for later calls (see
-    bq_kv_attn_workspace); allocated here when None."""
+    last `window` of them, and the first `sinks` of the sequence; else every
+    token held.  workspace: a uint8 tensor, zero before its first use and kept
+    for later calls (see bq_kv_attn_workspace); allocated here when None."""
+    window = _window(window, "window")
+    if not sinks:
+        return _attn("bq_kv_attn", cache, layer, q, cu, lens, table, scale, out, workspace, (), (window, KV_CAUSAL if causal else 0))
+    if not causal:
+        raise ValueError("sinks need causal")
+    return _attn("bq_kv_attn_sinks", cache, layer, q, cu, lens, table, scale, out, workspace, (), (window, _window(sinks, "sinks")))
+
+
+def kv_attn_tree(cache: KVCache, layer: int, q, cu, lens, table, mask, scale: Optional[float] = None, window: int = 0,
+                 sinks: int = 0, out=None, workspace=None):
+    """kv_attn() where the rows of each sequence are a tree of drafted tokens:
+    mask int64 [total][words] (tree_plan() makes it) says which rows of its
+    sequence a row sees, beside the context ahead of them (window > 0: the
+    last window less the rows it sees, and the first `sinks`)."""
+    dev = cache.device
+    _torch or _use_torch()
+    _need(mask, "mask", _torch.int64, dev)
+    if mask.dim() != 2 or mask.shape[0] != q.shape[0]:
+        raise ValueError(f"mask has shape {tuple(mask.shape)}, expected [{q.shape[0]}][words]")
+    return _attn("bq_kv_attn_tree", cache, layer, q, cu, lens, table, scale, out, workspace, (mask.data_ptr(), mask.shape[1]),
+                 (_window(window, "window"), _window(sinks, "sinks")))
+
+
+def _window(value, name):
+    return _int(min(value, (1 << 31) - 1), name)
+
+
+def _attn(name, cache, layer, q, cu, lens, table, scale, out, workspace, mask, seen):
     dev = cache.device
     stride = _rows(q, "q", dev, None, cache.head_dim)
     total, heads, dim = q.shape
@@ -344,10 +430,25 @@ def kv_attn(cache: KVCache, layer: int, q, cu, lens, table, scale: Optional[floa
         ws_bytes = workspace.numel()
     if workspace is not None:
         ws = workspace.data_ptr()
-    _launch(dev, "bq_kv_attn", cache.desc, _int(layer, "layer"), q.data_ptr(), out.data_ptr(), stride, out_stride, heads,
-            cu.data_ptr(), lens.data_ptr(), table.data_ptr(), batch, max_pages, total, dim ** -0.5 if scale is None else scale,
-            _int(min(window, (1 << 31) - 1), "window"), KV_CAUSAL if causal else 0, ws, ws_bytes)
+    _launch(dev, name, cache.desc, _int(layer, "layer"), q.data_ptr(), out.data_ptr(), stride, out_stride, heads,
+            cu.data_ptr(), lens.data_ptr(), table.data_ptr(), batch, max_pages, total, *mask,
+            dim ** -0.5 if scale is None else scale, *seen, ws, ws_bytes)
     return out
+
+
+def kv_keep(cache: KVCache, cu, lens, table, path, kept) -> None:
+    """Moves, over all layers, the keys and values of the rows path[b][i], i <
+    kept[b], of each sequence's last cu[b+1] - cu[b] tokens to the places of
+    the rows i (path int32 [batch][max_path], kept int32 [batch], as
+    tree_accept() gives them).  kv_resize() to its `want` then cuts the rest."""
+    dev = cache.device
+    batch, max_pages = _batch(cu, lens, table, dev)
+    _need(path, "path", _torch.int32, dev)
+    if path.dim() != 2 or path.shape[0] != batch:
+        raise ValueError(f"path has shape {tuple(path.shape)}, expected [{batch}][max_path]")
+    _ints(kept, "kept", dev, batch)
+    _launch(dev, "bq_kv_keep", cache.desc, cu.data_ptr(), lens.data_ptr(), table.data_ptr(), batch, max_pages,
+            path.data_ptr(), path.shape[1], kept.data_ptr())
 
 
 def _ints(t, name, device, *shape):
@@ -425,7 +526,9 @@ def kv_copy_pages(cache: KVCache, src, dst) -> None:
 
 __all__ = [
     "KV_ATTN_COUNTER_BYTES", "KV_BLOCK", "KV_CAUSAL", "KV_E4M3", "KV_FORMATS", "KV_I8", "KV_PAGE", "KV_POINTS",
-    "KVCache", "KVCacheDesc", "ROPE_ADJACENT", "ROPE_MAX_AXES", "bq_kv_append", "bq_kv_attn", "bq_kv_attn_workspace",
-    "bq_kv_compact", "bq_kv_copy_pages", "bq_kv_fork", "bq_kv_pages_workspace", "bq_kv_read", "bq_kv_resize",
-    "bq_rope", "kv_append", "kv_attn", "kv_compact", "kv_copy_pages", "kv_fork", "kv_read", "kv_resize", "rope",
+    "KVCache", "KVCacheDesc", "ROPE_ADJACENT", "ROPE_MAX_AXES", "TREE_MAX_ROWS", "TREE_MAX_WORDS", "bq_kv_append",
+    "bq_kv_append_norm", "bq_kv_attn", "bq_kv_attn_sinks", "bq_kv_attn_tree", "bq_kv_attn_workspace", "bq_kv_compact",
+    "bq_kv_copy_pages", "bq_kv_fork", "bq_kv_keep", "bq_kv_pages_workspace", "bq_kv_read", "bq_kv_resize",
+    "bq_norm_rope", "bq_rope", "kv_append", "kv_append_norm", "kv_attn", "kv_attn_tree", "kv_compact", "kv_copy_pages",
+    "kv_fork", "kv_keep", "kv_read", "kv_resize", "norm_rope", "rope",
 ]

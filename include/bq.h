@@ -469,6 +469,127 @@ int bq_kv_compact(const bq_kv_cache* cache, int* table, int* refs, int rows, int
                   void* workspace, size_t workspace_bytes, void* stream);
 int bq_kv_copy_pages(const bq_kv_cache* cache, const int* src, const int* dst, int n, void* stream);
 
+/* ------------------------------------------------------------------------
+ * A decoding step with a tree of drafted tokens, over the cache above.
+ *
+ * The tree of sequence b is its rows cu[b] .. cu[b+1] - 1: row 0 the last
+ * token decided, every other row a drafted token behind its parent row.
+ * parent, token and target are int32 [total] in device memory; parent[row] is
+ * a row's number in its sequence, smaller than the row's own, or -1: a row
+ * behind the context itself.  Any other value counts as -1.  Up to
+ * BQ_TREE_MAX_ROWS rows of a sequence.  As above, arrays are read by the
+ * kernels only, and what does not fit is never followed. */
+#define BQ_TREE_MAX_WORDS 16
+#define BQ_TREE_MAX_ROWS 1024
+
+/* norm_rope -- a norm of each head's row and the rotation of bq_rope in one
+ * pass: x * weight / sqrt(mean(x^2) + eps) over the head's dimensions, then
+ * turned; fp32 inside, rounded once.  weight fp32 [head_dim], eps >= 0 and
+ * finite (BQ_ERR_SHAPE); the rest as bq_rope, rot_dim 0 included (a norm
+ * alone).  y may be x.  A row of zeros with eps 0, and a row that holds an
+ * infinity or no number, give what the formula gives.
+ *
+ * kv_append_norm -- bq_kv_append with k normed by k_weight and q by q_weight
+ * ahead of the rotation (each fp32 [head_dim], or NULL: not normed). */
+int bq_norm_rope(const void* x, void* y, long long x_stride, long long y_stride, int tokens, int heads, int head_dim,
+                 const float* weight, float eps, const int* pos, const float* inv_freq, const int* axis, int rot_dim,
+                 int axes, int flags, void* stream);
+int bq_kv_append_norm(const bq_kv_cache* cache, int layer, const void* k, const void* v, long long k_stride,
+                      long long v_stride, const void* q, void* q_out, long long q_stride, long long q_out_stride,
+                      int q_heads, const int* cu, const int* lens, const int* table, int batch, int max_pages,
+                      int total, const float* k_weight, const float* q_weight, float eps, const int* pos,
+                      const float* inv_freq, const int* axis, int rot_dim, int axes, int flags, void* stream);
+
+/* kv_attn_sinks -- bq_kv_attn with BQ_KV_CAUSAL, where a row at position n
+ * sees beside the window's tokens the first `sinks` of its sequence: j <= n
+ * and (j > n - window or j < sinks).  window 0: all j <= n.  Pages that no row
+ * sees are not read.
+ *
+ * kv_attn_tree -- bq_kv_attn where each sequence's rows are a tree: row i of n
+ * sees the rows j of its sequence whose bit j % 64 of mask[row][j / 64] is set
+ * (its own among them, if it is to see itself; bits from n on do not count),
+ * and the context, the lens[b] - n tokens ahead of the tree: all of it, or
+ * with window > 0 the last window - (rows it sees of the tree) of its tokens
+ * and the first `sinks`.  mask uint64 [total][mask_words], 8-byte aligned, 1
+ * <= mask_words <= BQ_TREE_MAX_WORDS; rows past 64 * mask_words of a sequence
+ * are seen by none.  A row that sees nothing gives zeros.  bq_tree_plan makes
+ * the masks of a tree; a mask need not be one of a tree.
+ *
+ * Both: arguments, workspace, numerics and errors otherwise as bq_kv_attn
+ * (sinks < 0: BQ_ERR_SHAPE). */
+int bq_kv_attn_sinks(const bq_kv_cache* cache, int layer, const void* q, void* out, long long q_stride,
+                     long long out_stride, int q_heads, const int* cu, const int* lens, const int* table, int batch,
+                     int max_pages, int total, float scale, int window, int sinks, void* workspace,
+                     size_t workspace_bytes, void* stream);
+int bq_kv_attn_tree(const bq_kv_cache* cache, int layer, const void* q, void* out, long long q_stride,
+                    long long out_stride, int q_heads, const int* cu, const int* lens, const int* table, int batch,
+                    int max_pages, int total, const void* mask, int mask_words, float scale, int window, int sinks,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* tree_plan -- of every row the rows that it sees, itself and those above it
+ * (with window > 0 only the nearest `window` of them), as mask uint64
+ * [total][mask_words] for bq_kv_attn_tree, and its position for the rotation,
+ * pos int32 [total]: lens[b] - n + the number of rows above it.  mask or pos
+ * may be NULL (not both).  Rows past 64 * mask_words of a sequence see
+ * nothing and stand at its first row's position.
+ *
+ * tree_accept -- the path that the target tokens take from row 0 on: of the
+ * rows whose parent is the last row taken, the first whose token is that
+ * row's target is taken next (rows behind it in the sequence only).  target[row]
+ * is the token that the target model has after the row: its most likely one
+ * (bq_logprobs) or one that the caller drew.  For each sequence:
+ *   path [batch][max_path]  the rows taken, rising, then -1; path[0] = 0
+ *   kept [batch]            their number, at most max_path
+ *   next_token [batch]      the target behind the last of them
+ *   want [batch]            lens[b] - n + kept, the length for bq_kv_resize
+ * A sequence without rows: kept 0, next_token -1, want lens[b].  Rows past
+ * BQ_TREE_MAX_ROWS are never taken.  1 <= max_path <= BQ_TREE_MAX_ROWS.
+ *
+ * kv_keep -- over all layers, keys and values of the rows path[b][i], i <
+ * kept[b], go to the places of the rows i: with bq_kv_resize to `want` they
+ * are then the sequence's last tokens.  A block that takes a token gets the
+ * largest of its own scale and its tokens' scales; its codes are brought to it
+ * (rne; unchanged when the scale did not grow), so every token that no other
+ * replaces keeps its value.  lens still counts all n rows.  A sequence whose
+ * path does not rise from row to row inside 0 .. n - 1 is left as it is; a row
+ * whose page is missing is not moved.  Pages that are written must not be
+ * shared (as for bq_kv_append). */
+int bq_tree_plan(const int* parent, const int* cu, const int* lens, int batch, int total, int mask_words, int window,
+                 void* mask, int* pos, void* stream);
+int bq_tree_accept(const int* target, const int* token, const int* parent, const int* cu, const int* lens, int batch,
+                   int total, int max_path, int* path, int* kept, int* next_token, int* want, void* stream);
+int bq_kv_keep(const bq_kv_cache* cache, const int* cu, const int* lens, const int* table, int batch, int max_pages,
+               const int* path, int max_path, const int* kept, void* stream);
+
+/* logprobs -- of each row of logits [rows][V] (fp16 or fp32; row_stride in
+ * elements, at least V; aligned to the element) under p = softmax(row):
+ *   logprob [rows][count]       log p of the given tokens (int32 [rows][count];
+ *                               a token outside 0 .. V - 1: -inf)
+ *   entropy [rows]              -sum p log p
+ *   top_tokens, top_logprobs    the `top` largest, [rows][top], in
+ *   [rows][top]                 bq_spec_decode_verify's order: equal values,
+ *                               lowest token first; -0 equals 0; NaN first
+ * fp32 and int32 arrays, 4-byte aligned; tokens and logprob may be NULL with
+ * count 0, entropy may be NULL, top_tokens and top_logprobs with top 0; at
+ * least one is asked for.  Sums in fp32, one read of the logits.  Logits of
+ * -inf have probability 0; with top > V the places behind V hold token -1 and
+ * -inf.  A row with a NaN or +inf, and one of -inf alone, has no
+ * probabilities: its logprob, entropy and top_logprobs are NaN, its top_tokens
+ * are by value all the same.  0 <= count <= BQ_LOGPROBS_MAX_COUNT, 0 <= top <=
+ * BQ_LOGPROBS_MAX_TOP, 0 <= rows < 2^24, 1 <= V < 2^28.
+ * workspace: as bq_kv_attn's (its first BQ_LOGPROBS_COUNTER_BYTES zero before
+ * the first use, zero again after every call; 16-byte aligned, NULL allowed):
+ * it lets several workgroups share a row; less than bq_logprobs_workspace
+ * gives says gives fewer of them.  Results may differ in the last bits by the
+ * split, and are the same on every call with the same arguments. */
+#define BQ_LOGPROBS_MAX_TOP 64
+#define BQ_LOGPROBS_MAX_COUNT 1024
+#define BQ_LOGPROBS_COUNTER_BYTES 65536
+int bq_logprobs_workspace(int rows, int V, int logits_dtype, int top, size_t* bytes);
+int bq_logprobs(const void* logits, int logits_dtype, long long row_stride, int rows, int V, const int* tokens,
+                int count, float* logprob, float* entropy, int top, int* top_tokens, float* top_logprobs,
+                void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -13,3 +13,5 @@ from .qmv_oracle import (T5_MAX_BYTE, abs_mass, algorithmic_bytes, bits_of, chec
 from .spec_oracle import spec_verify, spec_verify_scalar, target_tokens
 from .kv_oracle import (PagesOracle, kv_append_f64, kv_attn_f64, kv_encode, kv_places, kv_sequence, kv_table,
                         rope_f64)
+from .tree_oracle import (causal_context, kv_attn_seen_f64, kv_keep_f64, logprobs_f64, norm_f64, tree_above,
+                          tree_accept, tree_context, tree_seen, tree_words)
