@@ -33,7 +33,7 @@ Split split_of(int rows, int V, int logits_dtype, int64_t room) {
   const int passes = (int)((blocks + kLpBlocks - 1) / kLpBlocks);
   int split = 1;
   if (rows > 0 && rows <= kLpSplitRows)
-    split = (int)std::min<int64_t>({(int64_t)(kTarget + rows - 1) / rows, passes, kLpMaxSplit, std::max<int64_t>(room / rows, 1)});
+    split = (int)std::min<int64_t>({std::max((kTarget + rows / 2) / rows, 1), passes, kLpMaxSplit, std::max<int64_t>(room / rows, 1)});
   const int each = (passes + split - 1) / split;
   return Split{(passes + each - 1) / each, each};
 }

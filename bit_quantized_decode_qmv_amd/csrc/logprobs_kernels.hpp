@@ -11,14 +11,20 @@
 // 2^((x - B) log2(e)).  A wave keeps one running maximum, sums are fp32, four to
 // a lane.
 //
-// The largest values: a value and its token make one 64-bit number (a larger
-// value first, then a lower token), all different.  A wave keeps its 64 largest
-// sorted across its lanes, a lane one.  A new one is found by comparing the
-// lane's maxima, which the softmax needs anyway, with the k-th largest that any
-// wave of the workgroup has so far, and goes to its place by one shift across
-// lanes; where many come at once (the first values, rows that rise) they are
-// sorted and the two lists merged.  So ties and order change nothing but the
-// time, and that by a bounded factor.
+// The largest values: a value and its token make one 64-bit number, a larger
+// value first, then a lower token, all different.  A wave collects numbers from
+// a floor on, below which none is among the `top`, in LDS, unsorted: a lane
+// compares its maximum, which the softmax needs anyway, and only where one
+// passes are the values of its 16-byte blocks that pass looked at, side by side,
+// a thread one (through LDS: a register has no number that a thread could
+// choose).  The floor begins at what
+// the maxima of a workgroup's first 1024 blocks say (`top` lanes hold a value
+// from it on, so as many values are), and rises when the room runs out: then
+// the `top` largest are found by bisection, a count over the wave for each
+// step, and the others leave.  In the end the waves' and the parts' numbers are
+// put together the same way, and each of the `top` finds its place by counting
+// those above it.  So ties and order change nothing but the time, and that by a
+// bounded factor.
 #pragma once
 
 #include "kv_common.hpp"
@@ -31,9 +37,10 @@ constexpr int kLpLoads = 4;                              // 16-byte loads of a l
 constexpr int kLpWaveBlocks = 64 * kLpLoads;             // 16-byte blocks a wave takes at a time
 constexpr int kLpBlocks = kLpWaves * kLpWaveBlocks;      // and a workgroup
 constexpr int kLpMaxSplit = 64;
-constexpr int kLpCounterStride = 16;                     // 4-byte words: a line of its own for each row
+constexpr int kLpCounterStride = 8;                      // 4-byte words between rows
 constexpr int kLpSplitRows = BQ_LOGPROBS_COUNTER_BYTES / (4 * kLpCounterStride);
-constexpr int kLpFew = 12;                               // new values that are put in one by one
+constexpr int kLpRoom = 256;                             // numbers a wave collects
+constexpr int kLpStage = 64;                             // blocks whose values it looks at
 
 struct LogprobsParams {
   const void* logits;
@@ -42,53 +49,178 @@ struct LogprobsParams {
   float *logprob, *entropy, *top_logprobs;
   int* top_tokens;
   unsigned* counters;  // workspace: parts done of each row, zero between calls
-  uint64_t* part;      // workspace: (m, B), (s, t), then `top` numbers, of each part
+  uint64_t* part;      // workspace: what the parts found
   int rows, V, count, top;
   int split;           // workgroups of a row
   int passes;          // of kLpBlocks that one of them makes
 };
-constexpr int lp_slot(int top) { return 2 + top; }  // 8-byte words of a part
+// 8-byte words of a part: (m, B), (s, t), up to 64 numbers, the largest first
+constexpr int lp_slot(int top) { return top > 0 ? 2 + 64 : 2; }
 
 typedef unsigned long long lp_key_t;
 
-// Larger first across the wave's lanes: one step of a sorting network.
-__device__ __forceinline__ lp_key_t lp_step(lp_key_t x, int d, bool up) {
-  const lp_key_t y = __shfl_xor(x, d, 64);
-  return (x > y) == up ? x : y;
+// The largest t found that at least `want` of some numbers reach (0 where fewer
+// reach 0), by distances below the largest of them: first powers of two, then
+// between two of them, until exactly `want` reach it or the steps run out.  A
+// step counts at three distances together: it is a chain of latencies, from the
+// lanes' comparison to the next distance, whatever it counts.
+template <typename Reach>
+__device__ __forceinline__ uint32_t lp_search(uint32_t largest, int want, int steps, Reach reach) {
+  const auto at = [&](uint32_t far) { return far < largest ? largest - far : 0u; };
+  // exponents: fewer than `want` reach a power that is `low`; at `high` enough do, or it is 2^32
+  int low = -1, high = 32;
+  while (high - low > 1) {
+    const int third = max((high - low) / 4, 1), a = low + third, b = min(a + third, high - 1), c = min(b + third, high - 1);
+    const int na = reach(at(1u << a)), nb = reach(at(1u << b)), nc = reach(at(1u << c));
+    if (na >= want) high = a;
+    else if (nb >= want) low = a, high = b;
+    else if (nc >= want) low = b, high = c;
+    else low = c;
+  }
+  uint32_t near = low < 0 ? 0u : 1u << low, far = high == 32 ? 0xFFFFFFFFu : 1u << high;
+  if (low < 0 && reach(largest) >= want) return largest;
+  for (int i = 0; i < steps && far - near > 1; ++i) {
+    const uint32_t part = max((far - near) >> 2, 1u), a = near + part, b = min(a + part, far - 1), c = min(b + part, far - 1);
+    const int na = reach(at(a)), nb = reach(at(b)), nc = reach(at(c));
+    int n = 0;
+    if (na >= want) far = a, n = na;
+    else if (nb >= want) near = a, far = b, n = nb;
+    else if (nc >= want) near = b, far = c, n = nc;
+    else near = c;
+    if (n == want) break;
+  }
+  return at(far);
 }
-// Sorts a sequence that rises and falls once (bitonic).
-__device__ __forceinline__ lp_key_t lp_merge_steps(lp_key_t x) {
-  const int lane = (int)threadIdx.x & 63;
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) x = lp_step(x, d, (lane & d) == 0);
-  return x;
+// A result over the wave's lanes in six steps of lanes nearby (data parallel
+// primitives: shifts within rows of 16, then broadcasts across rows); each lane
+// takes `none` where its neighbour lies outside.
+template <typename Op>
+__device__ __forceinline__ uint32_t lp_over_wave(uint32_t x, uint32_t none, Op op) {
+  x = op(x, __builtin_amdgcn_update_dpp(none, x, 0x111, 0xF, 0xF, false));  // row_shr:1
+  x = op(x, __builtin_amdgcn_update_dpp(none, x, 0x112, 0xF, 0xF, false));
+  x = op(x, __builtin_amdgcn_update_dpp(none, x, 0x114, 0xF, 0xF, false));
+  x = op(x, __builtin_amdgcn_update_dpp(none, x, 0x118, 0xF, 0xF, false));
+  x = op(x, __builtin_amdgcn_update_dpp(none, x, 0x142, 0xA, 0xF, false));  // row_bcast:15 into rows 1 and 3
+  x = op(x, __builtin_amdgcn_update_dpp(none, x, 0x143, 0xC, 0xF, false));  // row_bcast:31 into rows 2 and 3
+  return __builtin_amdgcn_readlane(x, 63);
 }
-__device__ __forceinline__ lp_key_t lp_sort(lp_key_t x) {
-  const int lane = (int)threadIdx.x & 63;
-#pragma unroll
-  for (int n = 2; n <= 64; n *= 2)
-#pragma unroll
-    for (int d = n >> 1; d > 0; d >>= 1) x = lp_step(x, d, ((lane & d) == 0) == ((lane & n) == 0 || n == 64));
-  return x;
+__device__ __forceinline__ uint32_t lp_wave_max(uint32_t x) {
+  return lp_over_wave(x, 0u, [](uint32_t a, uint32_t b) { return max(a, b); });
 }
-// The 64 largest of two sorted lists, sorted.
-__device__ __forceinline__ lp_key_t lp_merge(lp_key_t a, lp_key_t b) {
-  const lp_key_t r = __shfl(b, 63 - ((int)threadIdx.x & 63), 64);
-  return lp_merge_steps(a > r ? a : r);
+__device__ __forceinline__ uint32_t lp_wave_min(uint32_t x) {
+  return lp_over_wave(x, 0xFFFFFFFFu, [](uint32_t a, uint32_t b) { return min(a, b); });
 }
+template <typename Op>
+__device__ __forceinline__ float lp_over_wave(float x, float none, Op op) {
+  return __builtin_bit_cast(float, lp_over_wave(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, none), [&](uint32_t a, uint32_t b) {
+    return __builtin_bit_cast(uint32_t, op(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)));
+  }));
+}
+__device__ __forceinline__ float lp_wave_sum(float x) {
+  return lp_over_wave(x, 0.f, [](float a, float b) { return a + b; });
+}
+
 __device__ __forceinline__ lp_key_t lp_lane(lp_key_t x, int lane) {
   const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)x, lane), hi = __builtin_amdgcn_readlane((uint32_t)(x >> 32), lane);
   return ((lp_key_t)hi << 32) | lo;
 }
-// x (the same on all lanes) to its place in a sorted list; the last one leaves.
-__device__ __forceinline__ lp_key_t lp_insert(lp_key_t list, lp_key_t x) {
-  const int place = __builtin_popcountll(__ballot(list > x)), lane = (int)threadIdx.x & 63;
-  // each lane's neighbour below (data parallel primitive: a shift over the wave)
-  const uint32_t lo = __builtin_amdgcn_update_dpp(0u, (uint32_t)list, 0x138, 0xF, 0xF, false);
-  const uint32_t hi = __builtin_amdgcn_update_dpp(0u, (uint32_t)(list >> 32), 0x138, 0xF, 0xF, false);
-  const lp_key_t up = ((lp_key_t)hi << 32) | lo;
-  return lane < place ? list : lane == place ? x : up;
-}
+
+// A wave's numbers in LDS.
+struct LpPicked {
+  lp_key_t* room;   // [kLpRoom]
+  int n;
+  lp_key_t floor;   // numbers below it are not among the `top`
+  float least;      // and its value
+
+  __device__ __forceinline__ void raise(lp_key_t to) {
+    to = lp_lane(to, 0);  // (the same for all lanes)
+    if (to <= floor) return;
+    floor = to;
+    least = __builtin_bit_cast(float, SpecBits<float>::value_of((uint32_t)(to >> 32)));
+  }
+  // What lanes write others read; all in one wave.
+  static __device__ __forceinline__ void settle() {
+    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+  // The lanes' numbers from the floor on join (0: none).
+  __device__ __forceinline__ void add(lp_key_t key, int top) {
+    uint64_t found = __ballot(key != 0 && key >= floor);
+    if (found == 0) return;
+    if (n > kLpRoom - 64) {
+      keep(top);
+      found = __ballot(key != 0 && key >= floor);
+    }
+    if (key != 0 && key >= floor)
+      room[n + __builtin_amdgcn_mbcnt_hi((uint32_t)(found >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)found, 0))] = key;
+    n += __builtin_popcountll(found);
+  }
+  // How many are larger than the lane's own (of at most 64).
+  __device__ __forceinline__ int place(lp_key_t key) const {
+    int above = 0;
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) above += room[i] > key;  // (the same for all lanes: one read)
+    return above;
+  }
+  // All but the `top` largest leave.
+  __device__ __forceinline__ void keep(int top) {
+    settle();
+    if (n <= top) return;
+    if (n <= 64) keep<1>(top);
+    else keep<kLpRoom / 64>(top);
+  }
+  template <int EACH>
+  __device__ __forceinline__ void keep(int top) {
+    lp_key_t key[EACH];
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+      const int at = (int)(threadIdx.x & 63) + 64 * i;
+      key[i] = at < n ? room[at] : 0;
+    }
+    // by value, then, of those that have the last value, by token
+    uint32_t largest = 0;
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) largest = max(largest, (uint32_t)(key[i] >> 32));
+    largest = lp_wave_max(largest);
+    const uint32_t value = lp_search(largest, top, 32, [&](uint32_t at) {
+      int reach = 0;
+#pragma unroll
+      for (int i = 0; i < EACH; ++i) reach += __builtin_popcountll(__ballot((uint32_t)(key[i] >> 32) >= at));
+      return reach;
+    });
+    int above = 0, reach = 0;
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+      reach += __builtin_popcountll(__ballot((uint32_t)(key[i] >> 32) >= value));
+      above += __builtin_popcountll(__ballot((uint32_t)(key[i] >> 32) > value));
+    }
+    uint32_t token = 0;
+    if (reach > top) {
+      uint32_t most = 0;
+#pragma unroll
+      for (int i = 0; i < EACH; ++i) most = max(most, (uint32_t)(key[i] >> 32) == value ? (uint32_t)key[i] : 0u);
+      token = lp_search(lp_wave_max(most), top - above, 32, [&](uint32_t at) {
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < EACH; ++i)
+          n += __builtin_popcountll(__ballot((uint32_t)(key[i] >> 32) == value && (uint32_t)key[i] >= at));
+        return n;
+      });
+    }
+    const lp_key_t t = ((lp_key_t)value << 32) | token;
+    settle();
+    n = 0;
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+      const uint64_t found = __ballot(key[i] >= t);
+      if (key[i] >= t)
+        room[n + __builtin_amdgcn_mbcnt_hi((uint32_t)(found >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)found, 0))] = key[i];
+      n += __builtin_popcountll(found);
+    }
+    settle();
+    raise(t);
+  }
+};
 
 // Maxima that are no number where an operand is none.
 __device__ __forceinline__ uint32_t lp_max3(uint32_t a, uint32_t b, uint32_t c, _Float16) {
@@ -143,32 +275,33 @@ __device__ __forceinline__ void lp_scale(float& s, float& t, float d, float f) {
 __device__ __forceinline__ float lp_max(float a, float b) {  // no number where one is none
   return a != a ? a : b != b ? b : __builtin_fmaxf(a, b);
 }
-// Joins what `n` neighbouring lanes hold; the same result on each.
+// Joins what the lanes hold (m -inf: nothing).
 template <typename T>
-__device__ __forceinline__ LpSums lp_join(LpSums x, int n) {
-  float m = x.m;
-  for (int d = n >> 1; d > 0; d >>= 1) m = lp_max(m, __shfl_xor(m, d, 64));
-  const float b = lp_base(m, T{}), d = lp_moved(x.b, b, T{});
+__device__ __forceinline__ LpSums lp_join(LpSums x) {
+  LpSums all;
+  all.m = lp_over_wave(x.m, -__builtin_inff(), [](float a, float b) { return lp_max(a, b); });
+  all.b = lp_base(all.m, T{});
+  const float d = lp_moved(x.b, all.b, T{});
   lp_scale(x.s, x.t, d, x.m == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(d));
-  x.m = m;
-  x.b = b;
-  for (int d = n >> 1; d > 0; d >>= 1) {
-    x.s += __shfl_xor(x.s, d, 64);
-    x.t += __shfl_xor(x.t, d, 64);
-  }
-  return x;
+  all.s = lp_wave_sum(x.s);
+  all.t = lp_wave_sum(x.t);
+  return all;
 }
 
 // One workgroup for a part of a row (of the whole row where rows fill the
-// chip); a row's parts are joined by the one that finishes last.  The loads of
-// a wave's next 4 KB are in flight while it works on the last.  Bound by HBM
+// chip); a row's parts are joined by the one that finishes last.  A wave takes
+// 4 KB at a time; what hides its loads is the other waves of its SIMD.  Bound by HBM
 // where rows are many, then by issue: of a value two conversions and sums, an
 // exponential and a share of the maxima.  Measured: MEASURED_LP.
 template <typename T, bool ENTROPY, bool TOP>
-__global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LogprobsParams p) {
+__global__ __launch_bounds__(kLpThreads, TOP ? 6 : 8) void logprobs_kernel(LogprobsParams p) {
   constexpr int EPV = 16 / (int)sizeof(T);  // values of a 16-byte block
-  __shared__ lp_key_t lists[kLpWaves][64];
-  __shared__ lp_key_t bound;  // no value below it is among the `top`
+  __shared__ lp_key_t room[TOP ? kLpWaves : 1][TOP ? kLpRoom : 1];
+  __shared__ __align__(16) u32x4_t stage[TOP ? kLpWaves : 1][TOP ? kLpStage : 1];
+  __shared__ short stage_of[TOP ? kLpWaves : 1][TOP ? kLpStage : 1];
+  __shared__ lp_key_t bound;        // the highest of the waves' floors
+  __shared__ uint32_t first[TOP ? kLpThreads : 1];
+  __shared__ int counts[kLpWaves];
   __shared__ LpSums sums[kLpWaves];
   __shared__ int last;
   const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -180,27 +313,17 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LogprobsParams p) 
   const int all = (int)(((int64_t)lead + p.V + EPV - 1) / EPV);
   const int from = part * p.passes * kLpBlocks, to = min(from + p.passes * kLpBlocks, all);
 
-  LpSums x{-__builtin_inff(), 0.f, 0.f, 0.f};
+  LpSums x{-__builtin_inff(), 0.f, 0.f, 0.f};  // (the same for all lanes)
   float s[kLpLoads] = {}, t[kLpLoads] = {};
-  lp_key_t list = 0, own_bound = 0;
-  float least = -__builtin_inff();  // the value of the bound
-  bool none = false;                // something is no number
-  if constexpr (TOP) {
-    if (threadIdx.x == 0) bound = 0;
-    __syncthreads();
-  }
-  u32x4_t next[kLpLoads];
-  const auto request = [&](int q0) {
-#pragma unroll
-    for (int j = 0; j < kLpLoads; ++j) next[j] = blocks[min(q0 + 64 * j + lane, all - 1)];
-  };
+  [[maybe_unused]] LpPicked picked{room[TOP ? wave : 0], 0, 0, -__builtin_inff()};
+  bool none = false;  // something is no number
   int q0 = from + wave * kLpWaveBlocks;
-  if (q0 < to) request(q0);
-  for (; q0 < to; q0 += kLpBlocks) {
+  const int q_first = q0;
+  // (with TOP all waves make the first pass, which has a barrier; past the part it finds nothing)
+  for (; q0 < to || (TOP && q0 == q_first); q0 += kLpBlocks) {
     u32x4_t w[kLpLoads];
 #pragma unroll
-    for (int j = 0; j < kLpLoads; ++j) w[j] = next[j];
-    request(q0 + kLpBlocks);
+    for (int j = 0; j < kLpLoads; ++j) w[j] = blocks[min(q0 + 64 * j + lane, all - 1)];
     const bool inside = q0 * EPV >= lead && (int64_t)(q0 + kLpWaveBlocks) * EPV - lead <= p.V && q0 + kLpWaveBlocks <= to;
     if (!inside) {
       // values outside the row, and blocks past the part, are -inf
@@ -224,9 +347,8 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LogprobsParams p) 
     const float top = lp_float(lp_max3(lp_max3(most[0], most[1], most[2], T{}), most[3], most[3], T{}), T{});
     none = none || top != top;
     if (__ballot(top > x.m) != 0) {
-      float m = __builtin_fmaxf(x.m, top);  // (a NaN counts for nothing here)
-#pragma unroll
-      for (int d = 32; d > 0; d >>= 1) m = __builtin_fmaxf(m, __shfl_xor(m, d, 64));
+      // (a NaN counts for nothing here)
+      const float m = lp_over_wave(__builtin_fmaxf(x.m, top), -__builtin_inff(), [](float a, float b) { return __builtin_fmaxf(a, b); });
       const float b = lp_base(m, T{}), d = lp_moved(x.b, b, T{});
       const float f = x.m == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(d);
 #pragma unroll
@@ -245,71 +367,89 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LogprobsParams p) 
         if constexpr (ENTROPY) t[j] = __builtin_fmaf(y, f, t[j]);
       }
     if constexpr (TOP) {
-      const lp_key_t others = *(volatile lp_key_t*)&bound;
-      if (others > own_bound) {
-        own_bound = others;
-        least = __builtin_bit_cast(float, SpecBits<float>::value_of((uint32_t)(own_bound >> 32)));
+      if (q0 == q_first) {
+        // `top` of the workgroup's lanes hold a value that reaches the floor
+        first[threadIdx.x] = q0 < to ? spec_key(top) : 0u;
+        if (threadIdx.x == 0) bound = 0;
+        __syncthreads();
+        uint32_t of[kLpWaves], largest = 0;
+#pragma unroll
+        for (int i = 0; i < kLpWaves; ++i) largest = max(largest, of[i] = first[64 * i + lane]);
+        // (few are found as well among the largest of four lanes each)
+        const uint32_t most_of = lp_wave_max(largest);
+        const uint32_t all = p.top <= 24 ? lp_search(most_of, p.top, 2, [&](uint32_t at) { return __builtin_popcountll(__ballot(largest >= at)); })
+                                         : lp_search(most_of, p.top, 2, [&](uint32_t at) {
+                                             int reach = 0;
+#pragma unroll
+                                             for (int i = 0; i < kLpWaves; ++i) reach += __builtin_popcountll(__ballot(of[i] >= at));
+                                             return reach;
+                                           });
+        picked.raise((lp_key_t)all << 32);
       }
-      if (__ballot(!(top < least)) != 0) {
-        const lp_key_t before = own_bound;
-        const auto raise = [&] {
-          const lp_key_t k = lp_lane(list, p.top - 1);
-          if (k > own_bound) {
-            own_bound = k;
-            least = __builtin_bit_cast(float, SpecBits<float>::value_of((uint32_t)(k >> 32)));
-          }
-        };
+      if (__ballot(!(top < picked.least)) != 0) {
+        picked.raise(*(volatile lp_key_t*)&bound);
+        const lp_key_t before = picked.floor;
+        // the blocks whose maximum passes go to LDS side by side, of all loads or, where they are many, of one
+        bool pass[kLpLoads];
+        uint64_t found[kLpLoads];
+        int blocks_found = 0;
 #pragma unroll
         for (int j = 0; j < kLpLoads; ++j) {
-          if (__ballot(!(lp_float(most[j], T{}) < least)) == 0) continue;
-          const int64_t v0 = (int64_t)(q0 + 64 * j + lane) * EPV - lead;
-          const bool here = q0 + 64 * j + lane < to;
-#pragma unroll
-          for (int e = 0; e < EPV; ++e) {
-            const float value = lp_value<T>(w[j], e);
-            if (__ballot(!(value < least)) == 0) continue;
-            const bool real = here && v0 + e >= 0 && v0 + e < p.V;
-            lp_key_t key = real ? spec_pack(spec_key(value), (int)(v0 + e)) : 0ull;
-            key = key > own_bound ? key : 0ull;
-            uint64_t found = __ballot(key != 0);
-            if (found == 0) continue;
-            if (__builtin_popcountll(found) > kLpFew) {
-              list = lp_merge(list, lp_sort(key));
-              raise();
-            } else {
-              for (; found != 0; found &= found - 1) {
-                const lp_key_t k = lp_lane(key, __builtin_ctzll(found));
-                if (k <= own_bound) continue;
-                list = lp_insert(list, k);
-                raise();
-              }
-            }
-          }
+          pass[j] = !(lp_float(most[j], T{}) < picked.least);
+          found[j] = __ballot(pass[j]);
+          blocks_found += __builtin_popcountll(found[j]);
         }
-        if (own_bound != before && lane == 0) atomicMax(&bound, own_bound);
+        const int loads = blocks_found <= kLpStage ? kLpLoads : 1;
+        for (int j0 = 0; j0 < kLpLoads; j0 += loads) {
+          int n = 0;
+#pragma unroll
+          for (int j = 0; j < kLpLoads; ++j) {
+            if (j < j0 || j >= j0 + loads) continue;
+            if (pass[j]) {
+              const int at = n + __builtin_amdgcn_mbcnt_hi((uint32_t)(found[j] >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)found[j], 0));
+              stage[TOP ? wave : 0][at] = w[j];
+              stage_of[TOP ? wave : 0][at] = 64 * j + lane;
+            }
+            n += __builtin_popcountll(found[j]);
+          }
+          LpPicked::settle();
+          // their values, a thread one
+          for (int i = lane / EPV; i - lane / EPV < n; i += 64 / EPV) {
+            const int at = min(i, n - 1), q = q0 + stage_of[TOP ? wave : 0][at];
+            const T value = reinterpret_cast<const T*>(&stage[TOP ? wave : 0][at])[lane % EPV];
+            const int64_t v = (int64_t)q * EPV + lane % EPV - lead;
+            picked.add(i < n && q < to && v >= 0 && v < p.V ? spec_pack(spec_key((float)value), (int)v) : 0ull, p.top);
+          }
+          LpPicked::settle();
+        }
+        if (picked.floor != before && lane == 0) atomicMax(&bound, picked.floor);
       }
     }
   }
   // the wave's sums, then the workgroup's
-  x.s = (s[0] + s[1]) + (s[2] + s[3]);
-  if constexpr (ENTROPY) x.t = (t[0] + t[1]) + (t[2] + t[3]);
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) {
-    x.s += __shfl_xor(x.s, d, 64);
-    if constexpr (ENTROPY) x.t += __shfl_xor(x.t, d, 64);
-  }
+  x.s = lp_wave_sum((s[0] + s[1]) + (s[2] + s[3]));
+  if constexpr (ENTROPY) x.t = lp_wave_sum((t[0] + t[1]) + (t[2] + t[3]));
   if (__ballot(none) != 0) x.m = __builtin_nanf("");
   if (lane == 0) sums[wave] = x;
-  if constexpr (TOP) lists[wave][lane] = list;
-  __syncthreads();
-  if (wave == 0) {
-    x = lp_join<T>(sums[lane & (kLpWaves - 1)], kLpWaves);
+  // wave 0 takes what the others collected, and leaves `most` of them
+  const auto gather = [&]([[maybe_unused]] int most) {
     if constexpr (TOP) {
-      list = lists[0][lane];
-#pragma unroll
-      for (int i = 1; i < kLpWaves; ++i) list = lp_merge(list, lists[i][lane]);
+      if (lane == 0) counts[wave] = picked.n;
     }
-  }
+    __syncthreads();
+    if constexpr (TOP) {
+      if (wave == 0) {
+        for (int i = 1; i < kLpWaves; ++i) {
+          const int n = __builtin_amdgcn_readfirstlane(counts[i]);
+          for (int at = 0; at < n; at += 64) picked.add(at + lane < n ? room[i][at + lane] : 0ull, p.top);
+        }
+        if (picked.n > most) picked.keep(p.top);
+      }
+    }
+  };
+  gather(p.split > 1 ? 64 : p.top);
+  const LpSums nothing{-__builtin_inff(), 0.f, 0.f, 0.f};
+  if (wave == 0) x = lp_join<T>(lane < kLpWaves ? sums[lane] : nothing);
   if (p.split > 1) {
     const int slot = lp_slot(p.top);
     uint64_t* mine = p.part + (int64_t)blockIdx.x * slot;
@@ -326,7 +466,11 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LogprobsParams p) 
         put(mine, pack(x.m, x.b));
         put(mine + 1, pack(x.s, x.t));
       }
-      if (TOP && lane < p.top) put(mine + 2 + lane, list);
+      if constexpr (TOP) {
+        picked.settle();
+        const lp_key_t key = lane < picked.n ? room[0][lane] : 0ull;
+        put(mine + 2 + (key != 0 ? picked.place(key) : lane), key);
+      }
       // the stores are performed at device scope before the count is
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       if (lane == 0)
@@ -334,31 +478,39 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LogprobsParams p) 
     }
     __syncthreads();
     if (!last) return;
-    // the row's parts, a lane each; their lists, a wave every fourth, in order
+    // the row's parts, a lane each; their numbers, a wave every fourth
     const uint64_t* parts = p.part + (int64_t)row * p.split * slot;
-    x = LpSums{-__builtin_inff(), 0.f, 0.f, 0.f};
-    if (wave == 0 && lane < p.split) {
-      const uint64_t a = get(parts + lane * slot), b = get(parts + lane * slot + 1);
-      x.m = __builtin_bit_cast(float, (uint32_t)a);
-      x.b = __builtin_bit_cast(float, (uint32_t)(a >> 32));
-      x.s = __builtin_bit_cast(float, (uint32_t)b);
-      x.t = __builtin_bit_cast(float, (uint32_t)(b >> 32));
-    }
+    const uint64_t* of = parts + min(lane, p.split - 1) * slot;
+    const uint64_t mb = get(of), st = get(of + 1);
     if constexpr (TOP) {
-      list = 0;
-      for (int i = wave; i < p.split; i += kLpWaves) {
-        const lp_key_t other = lane < p.top ? get(parts + i * slot + 2 + lane) : 0ull;
-        list = i == wave ? other : lp_merge(list, other);
-      }
-      lists[wave][lane] = list;
-      __syncthreads();
-    }
-    if (wave == 0) {
-      x = lp_join<T>(x, 64);
-      if constexpr (TOP) {
+      // Each part but the last has `top` numbers at least, so `top` reach the lowest of their q-th ones.
+      const int q = (p.top + p.split - 2) / (p.split - 1);
+      const uint64_t qth = get(parts + min(lane, p.split - 2) * slot + 2 + q - 1);
+      constexpr int AHEAD = 5;
+      lp_key_t key[AHEAD];
+      const auto ask = [&](int i0) {
 #pragma unroll
-        for (int i = 1; i < kLpWaves; ++i) list = lp_merge(list, lists[i][lane]);
+        for (int k = 0; k < AHEAD; ++k) key[k] = get(parts + min(i0 + k * kLpWaves, p.split - 1) * slot + 2 + lane);
+      };
+      ask(wave);
+      picked = LpPicked{room[wave], 0, 0, -__builtin_inff()};
+      picked.raise((lp_key_t)lp_wave_min((uint32_t)(qth >> 32)) << 32);
+      for (int i0 = wave; i0 < p.split; i0 += AHEAD * kLpWaves) {
+        if (i0 != wave) ask(i0);
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) picked.add(i0 + k * kLpWaves < p.split ? key[k] : 0ull, p.top);
       }
+    }
+    gather(p.top);
+    if (wave == 0) {
+      x = nothing;
+      if (lane < p.split) {
+        x.m = __builtin_bit_cast(float, (uint32_t)mb);
+        x.b = __builtin_bit_cast(float, (uint32_t)(mb >> 32));
+        x.s = __builtin_bit_cast(float, (uint32_t)st);
+        x.t = __builtin_bit_cast(float, (uint32_t)(st >> 32));
+      }
+      x = lp_join<T>(x);
     }
     if (threadIdx.x == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
@@ -370,10 +522,17 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LogprobsParams p) 
   const bool fine = x.m > -__builtin_inff() && x.m < __builtin_inff();
   const float log_s = logf(x.s), shift = fine ? log_s - lp_rounding(x.m, x.b, T{}) : nan;
   if (ENTROPY && threadIdx.x == 0) p.entropy[row] = fine ? log_s - kLn2 * (x.t / x.s) : nan;
-  if (TOP && wave == 0 && lane < p.top) {
-    const float value = __builtin_bit_cast(float, SpecBits<float>::value_of((uint32_t)(list >> 32)));
-    p.top_tokens[(int64_t)row * p.top + lane] = list != 0 ? (int)(0xFFFFFFFFu - (uint32_t)list) : -1;
-    p.top_logprobs[(int64_t)row * p.top + lane] = list != 0 ? (value - x.m) - shift : -__builtin_inff();
+  if constexpr (TOP) {
+    if (wave == 0) {
+      const lp_key_t key = lane < picked.n ? room[0][lane] : 0ull;
+      int place = picked.place(key);
+      if (lane < p.top) {
+        if (lane >= picked.n) place = lane;  // behind the vocabulary
+        const float value = __builtin_bit_cast(float, SpecBits<float>::value_of((uint32_t)(key >> 32)));
+        p.top_tokens[(int64_t)row * p.top + place] = key != 0 ? (int)(0xFFFFFFFFu - (uint32_t)key) : -1;
+        p.top_logprobs[(int64_t)row * p.top + place] = key != 0 ? (value - x.m) - shift : -__builtin_inff();
+      }
+    }
   }
   for (int i = (int)threadIdx.x; i < p.count; i += kLpThreads) {
     const int token = p.tokens[(int64_t)row * p.count + i];
