@@ -218,6 +218,38 @@ __device__ __forceinline__ bool kv_attn_work(const P& p, int item, KvWork& w) {
     // 2047 pages has parts of 20 pages, 103 of them, 26 us.)
     const unsigned share = ROWS <= 32 ? (unsigned)all + (unsigned)all / 4 : (unsigned)all;
     w.chunk = max((int)((share + p.target - 1) / (unsigned)p.target), least);
+    if constexpr (ROWS > 32 && std::is_same_v<P, KvAttnMore>) {
+      // Many rows of a tree, or with sinks: no more than 32 parts of a tile on
+      // average, and two pages each (min_pages).  Measured, us with parts of 2,
+      // 4 and 8 pages: one tree of 13 rows of 48 heads over 1003 tokens 14.4,
+      // 17.6 and 23.1, over 4000 17.9, 18.8 and 23.2, four trees over up to
+      // 2000 17.8, 18.8 and 23.8; 61 rows of 16 heads of 64 over 16000 (250
+      // pages) 27.4, 27.7 and 24.1.
+      int count = 0;
+      for (int base = 0; base < batch; base += 64) count += __builtin_amdgcn_readlane(kv_scan(tiles(seq(base))), 63);
+      const unsigned most = 32u * (unsigned)max(count, 1);
+      w.chunk = max(w.chunk, (int)(((unsigned)all + most - 1) / most));
+      // From 12 pages on somewhat longer parts, if all of them then run at
+      // once.  Measured, us without and with that: 64 rows of 48 heads over
+      // 131001 tokens 250 and 233, 61 rows over 60000 129 and 118, of eight
+      // sequences of up to 30000 202 and 180, 13 rows of twelve of up to 16000
+      // 74 and 59.
+      if (w.chunk >= 12) {
+        const int first = w.chunk;
+        w.chunk = first + (first + 15) / 16;
+        for (int i = 0; i < 6; ++i) {
+          const int c = first + i * max(first / 48, 1);
+          int parts = 0;
+          for (int base = 0; base < batch; base += 64) {
+            const KvSeq s = seq(base);
+            parts += __builtin_amdgcn_readlane(kv_scan(tiles(s) * ((int)((unsigned)(pages(s) - 1) / (unsigned)c) + 1)), 63);
+          }
+          if (parts > p.target) continue;
+          w.chunk = c;
+          break;
+        }
+      }
+    }
   }
   // whole parts ahead of a tile's last one
   const auto whole = [&](const KvSeq& s) { return (int)((unsigned)(pages(s) - 1) / (unsigned)w.chunk); };

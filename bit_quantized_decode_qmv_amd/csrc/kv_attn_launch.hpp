@@ -56,7 +56,8 @@ struct KvAttnPlan {
   int64_t tiles, target;
   size_t bytes;
 };
-inline KvAttnPlan kv_attn_plan(const bq_kv_cache* c, int q_heads, int batch, int total, int64_t max_pages, size_t workspace_bytes) {
+template <typename P>
+KvAttnPlan kv_attn_plan(const bq_kv_cache* c, int q_heads, int batch, int total, int64_t max_pages, size_t workspace_bytes) {
   KvAttnPlan p{};
   // By the rows of a sequence, on average; two row groups of wide heads do
   // not fit a wave's registers.  Tiles of 32 for up to 128 rows instead:
@@ -137,14 +138,14 @@ int kv_attn_run(P p, const bq_kv_cache* cache, int layer, const void* q, void* o
   p.causal = flags & BQ_KV_CAUSAL;
   p.window = std::min(window, 1 << 30);  // no sequence is longer; a row's place may be negative
   p.scale = scale * 1.44269504f;
-  const KvAttnPlan pl = kv_attn_plan(cache, q_heads, batch, total, max_pages, workspace ? workspace_bytes : 0);
+  const KvAttnPlan pl = kv_attn_plan<P>(cache, q_heads, batch, total, max_pages, workspace ? workspace_bytes : 0);
   p.target = (int)pl.target;
   // (many rows, measured: parts of 4 pages are 17% faster than of 8 at D 64,
   // 13% slower at D 128.  Wide heads, 4 with 6 query heads each, us in parts of
   // 4, 8 and 16 pages: 40 rows of 2 sequences of up to 4000 tokens, D 256, 34.2,
   // 39.8 and 56.1, D 192 29.3, 33.5 and 47.2; 100 rows over 8000, D 256, 66.5,
   // 66.5 and 60.1; five rows of 8 sequences of up to 16000 67.5, 67.5 and 58.3)
-  p.min_pages = pl.rows < kPromptRows ? 0 : D == 64 ? 4 : 8;
+  p.min_pages = pl.rows < kPromptRows ? 0 : std::is_same_v<P, KvAttnMore> ? 2 : D == 64 ? 4 : 8;
   p.counters = static_cast<unsigned*>(workspace);
   p.part = workspace ? reinterpret_cast<float*>(static_cast<char*>(workspace) + BQ_KV_ATTN_COUNTER_BYTES) : nullptr;
   const int64_t wgs = pl.tiles + pl.target;

@@ -424,11 +424,12 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
   }
 }
 
-// Joins the parts of the tiles that have several, in order; a workgroup takes
-// 16 rows of a tile.
+// Joins the parts of the tiles that have several, in order; a workgroup takes 16
+// rows of a tile, 16 lanes one of them.  Bound by the latency of its reads, so
+// several parts are asked for at a time.
 template <int D, typename P>
 __global__ __launch_bounds__(256) void kv_attn_join_kernel(P p) {
-  constexpr int SLOT = kv_part_floats(kPromptRows, D);
+  constexpr int SLOT = kv_part_floats(kPromptRows, D), C = D / 64;
   __shared__ float f[kKvMaxParts][16];
   const int head = (int)blockIdx.x, item = (int)blockIdx.y / (kPromptRows / 16), first = (int)blockIdx.y % (kPromptRows / 16) * 16;
   KvWork w;
@@ -459,15 +460,39 @@ __global__ __launch_bounds__(256) void kv_attn_join_kernel(P p) {
   if (row >= some) return;
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
   const int token = (row0 + row) / p.group, qh = head * p.group + row0 + row - token * p.group;
-  _Float16* dst = p.out + (int64_t)(s.q0 + token) * p.out_stride + qh * D;
+  _Float16* dst = p.out + (int64_t)(s.q0 + token) * p.out_stride + qh * D + 4 * sub;
+  f32x4 y[C];
 #pragma unroll
-  for (int d = 4 * sub; d < D; d += 64) {
-    f32x4 y = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int i = 0; i < w.parts; ++i)
-      y += *reinterpret_cast<const f32x4*>(part0 + i * next + 2 * kPromptRows + (first + row) * D + d) * f[i][row];
-    y *= inv;
-    *reinterpret_cast<half4_t*>(dst + d) = half4_t{(_Float16)y[0], (_Float16)y[1], (_Float16)y[2], (_Float16)y[3]};
+  for (int c = 0; c < C; ++c) y[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const float* mine = part0 + 2 * kPromptRows + (first + row) * D + 4 * sub;
+  // several at a time, and what is left two at a time, the last one's again for one that is not there
+  const auto add = [&](int i0, auto ahead) {
+    constexpr int AHEAD = decltype(ahead)::value;
+    constexpr bool ALL = AHEAD > 2;
+    f32x4 v[AHEAD][C];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        v[k][c] = *reinterpret_cast<const f32x4*>(mine + (ALL ? i0 + k : min(i0 + k, w.parts - 1)) * next + 64 * c);
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      const float by = f[ALL ? i0 + k : min(i0 + k, w.parts - 1)][row];
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const f32x4 more = y[c] + v[k][c] * by;
+        y[c] = ALL || i0 + k < w.parts ? more : y[c];
+      }
+    }
+  };
+  constexpr int MANY = D <= 128 ? 8 : 4;
+  int i0 = 0;
+  for (; i0 + MANY <= w.parts; i0 += MANY) add(i0, std::integral_constant<int, MANY>{});
+  for (; i0 < w.parts; i0 += 2) add(i0, std::integral_constant<int, 2>{});
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    y[c] *= inv;
+    *reinterpret_cast<half4_t*>(dst + 64 * c) = half4_t{(_Float16)y[c][0], (_Float16)y[c][1], (_Float16)y[c][2], (_Float16)y[c][3]};
   }
 }
 

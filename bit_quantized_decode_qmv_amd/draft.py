@@ -110,10 +110,11 @@ def tree_accept(target, token, parent, cu, lens, max_path: int):
     if not 1 <= max_path <= _kv.TREE_MAX_ROWS:
         raise ValueError(f"max_path = {max_path}, expected 1 .. {_kv.TREE_MAX_ROWS}")
     path = torch.empty((batch, max_path), dtype=torch.int32, device=dev)
-    kept, after, want = torch.empty((3, batch), dtype=torch.int32, device=dev)
+    told = torch.empty((3, batch), dtype=torch.int32, device=dev)
+    at = told.data_ptr()
     _kv._launch(dev, "bq_tree_accept", target.data_ptr(), token.data_ptr(), parent.data_ptr(), cu.data_ptr(),
-                lens.data_ptr(), batch, total, max_path, path.data_ptr(), kept.data_ptr(), after.data_ptr(), want.data_ptr())
-    return path, kept, after, want
+                lens.data_ptr(), batch, total, max_path, path.data_ptr(), at, at + 4 * batch, at + 8 * batch)
+    return path, *told.unbind()
 
 
 def logprobs(logits, tokens=None, top: int = 0, entropy: bool = False, workspace=None):
