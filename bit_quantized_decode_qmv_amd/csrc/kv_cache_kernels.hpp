@@ -171,6 +171,23 @@ __host__ __device__ inline int norm_lanes(int head_dim) {
   return lanes;
 }
 
+// The sum over groups of `lanes` lanes, the same bits on each: within 16 by data
+// parallel primitives (neighbours, pairs, then mirrors, whose lanes hold equal
+// sums by then).
+template <int CTL>
+__device__ __forceinline__ float norm_add(float x) {
+  return x + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTL, 0xF, 0xF, false));
+}
+__device__ __forceinline__ float norm_sum(float x, int lanes) {
+  if (lanes >= 2) x = norm_add<0xB1>(x);    // quad_perm [1, 0, 3, 2]
+  if (lanes >= 4) x = norm_add<0x4E>(x);    // quad_perm [2, 3, 0, 1]
+  if (lanes >= 8) x = norm_add<0x141>(x);   // row_half_mirror
+  if (lanes >= 16) x = norm_add<0x140>(x);  // row_mirror
+  if (lanes >= 32) x += __shfl_xor(x, 16, 64);
+  if (lanes >= 64) x += __shfl_xor(x, 32, 64);
+  return x;
+}
+
 // rope_rows with a norm: a thread's unit is the same in all of its rounds
 // (a round is a multiple of 64 threads), so its sixteen weights stay in
 // registers, and a row's sum of squares is the work of `lanes` lanes side by
@@ -219,8 +236,7 @@ __device__ __forceinline__ void norm_rope_rows(const RopeRows& p, const RopeAngl
       }
 #pragma unroll
       for (int j = 0; j < 16; ++j) sum = __builtin_fmaf(y[j], y[j], sum);
-      sum = mine ? sum : 0.f;
-      for (int o = lanes >> 1; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
+      sum = norm_sum(mine ? sum : 0.f, lanes);
       const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(sum, mean, norm.eps));
       if (!mine || i0 + k * threads >= all) continue;
 #pragma unroll
@@ -287,9 +303,9 @@ __device__ __forceinline__ void kv_transpose4(const uint32_t (&x)[4], uint32_t (
 // Long calls are bound by HBM, short ones by the chain of latencies from the
 // table to the page.  Measured, 8 heads of 128 and q of 48: 4093 tokens 30 us
 // (4.2 TB/s), one token each of 32 sequences 7.7 us.
-// NORM: a token's units lie on D / 16 threads side by side, of two waves where
-// D is 192; their sums of squares are exchanged through LDS ahead of the
-// barrier that the angles' table needs anyway.
+// NORM: a token's units lie on D / 16 threads side by side; where D is 192 they
+// may be of two waves, and the sums of squares are exchanged through LDS ahead
+// of the barrier that the angles' table needs anyway.
 template <int PER, bool NORM = false>
 __global__ __launch_bounds__(PER == 4 ? 512 : 1024) void kv_append_kernel(
     std::conditional_t<NORM, KvAppendNormParams, KvAppendParams> p) {
@@ -297,6 +313,7 @@ __global__ __launch_bounds__(PER == 4 ? 512 : 1024) void kv_append_kernel(
   __shared__ __align__(16) uint8_t codes[2][kKvPage * 256];
   __shared__ RopeFreq freq[128];
   __shared__ int axis[128], pos[BQ_ROPE_MAX_AXES][kKvPage];
+  __shared__ __align__(16) float weight[NORM ? 256 : 1];
   const int D = p.head_dim, units = D >> 4;
   if ((int)blockIdx.x >= p.items) {
     const int t0 = ((int)blockIdx.x - p.items) * p.q_tokens_per_wg;
@@ -367,29 +384,27 @@ __global__ __launch_bounds__(PER == 4 ? 512 : 1024) void kv_append_kernel(
     }
   }
   const bool turns = !which && unit < (p.a.rot >> 4);
-  [[maybe_unused]] float w[16];
+  [[maybe_unused]] float root[PER];  // a token's sum of squares
   [[maybe_unused]] float(*squares)[kKvBlock][17] = nullptr;  // [block][token][unit], in LDS that the codes take later
   [[maybe_unused]] bool norms = false;
   if constexpr (NORM) {
     norms = !which && p.k_norm.w;
     squares = reinterpret_cast<float(*)[kKvBlock][17]>(&codes[1][0]);
+    if (p.k_norm.w)
+      for (int i = (int)threadIdx.x; i < D; i += (int)blockDim.x) weight[i] = p.k_norm.w[i];
     if (norms) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        w[j] = p.k_norm.w[lo + j];
-        w[8 + j] = p.k_norm.w[hi + j];
-      }
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         const int t = t00 + (i0 + i) * kKvBlock + tok;
-        if (t < start || t >= s.len) continue;
+        const bool fresh = t >= start && t < s.len;
         float sum = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float a = (float)raw[i][0][j], b = (float)raw[i][1][j];
           sum = __builtin_fmaf(a, a, __builtin_fmaf(b, b, sum));
         }
-        squares[i0 + i][tok][unit] = sum;
+        if (units != 12) root[i] = norm_sum(fresh ? sum : 0.f, units);
+        else if (fresh) squares[i0 + i][tok][unit] = sum;
       }
     }
   }
@@ -418,11 +433,19 @@ __global__ __launch_bounds__(PER == 4 ? 512 : 1024) void kv_append_kernel(
       }
       if constexpr (NORM) {
         if (norms) {
-          float sum = 0.f;
-          for (int u = 0; u < units; ++u) sum += squares[i0 + i][tok][u];
+          float sum = root[i];
+          if (units == 12) {
+            sum = 0.f;
+#pragma unroll
+            for (int u = 0; u < 12; ++u) sum += squares[i0 + i][tok][u];
+          }
           const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(sum, 1.f / (float)D, p.k_norm.eps));
 #pragma unroll
-          for (int j = 0; j < 16; ++j) x[i][j] *= r * w[j];
+          for (int j = 0; j < 16; j += 4) {
+            const f32x4 w = *reinterpret_cast<const f32x4*>(&weight[j < 8 ? lo + j : hi + j - 8]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[i][j + k] *= r * w[k];
+          }
         }
       }
       if (turns) {
