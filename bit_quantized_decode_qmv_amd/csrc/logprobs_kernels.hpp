@@ -19,9 +19,10 @@
 // a thread one (through LDS: a register has no number that a thread could
 // choose).  The floor begins at what
 // the maxima of a workgroup's first 1024 blocks say (`top` lanes hold a value
-// from it on, so as many values are), and rises when the room runs out: then
-// the `top` largest are found by bisection, a count over the wave for each
-// step, and the others leave.  In the end the waves' and the parts' numbers are
+// from it on, so as many values are), rises by a wave's maxima where most of
+// its lanes pass, and when the room runs out: then the `top` largest are found
+// by bisection, a count over the wave for each step, and the others leave.  A
+// value equal to the floor's passes only with a lower token.  In the end the waves' and the parts' numbers are
 // put together the same way, and each of the `top` finds its place by counting
 // those above it.  So ties and order change nothing but the time, and that by a
 // bounded factor.
@@ -130,14 +131,19 @@ struct LpPicked {
   lp_key_t* room;   // [kLpRoom]
   int n;
   lp_key_t floor;   // numbers below it are not among the `top`
-  float least;      // and its value
+  float least;      // its value
+  float above;      // and the next larger one, which a later token than the floor's needs (NaN: all pass)
 
   __device__ __forceinline__ void raise(lp_key_t to) {
     to = lp_lane(to, 0);  // (the same for all lanes)
     if (to <= floor) return;
     floor = to;
-    least = __builtin_bit_cast(float, SpecBits<float>::value_of((uint32_t)(to >> 32)));
+    const uint32_t key = (uint32_t)(to >> 32);
+    least = __builtin_bit_cast(float, SpecBits<float>::value_of(key));
+    above = __builtin_bit_cast(float, SpecBits<float>::value_of(key + 1));
   }
+  // What a value of these tokens, the first of them `first`, has to reach.
+  __device__ __forceinline__ float limit(int first) const { return (uint32_t)first > 0xFFFFFFFFu - (uint32_t)floor ? above : least; }
   // What lanes write others read; all in one wave.
   static __device__ __forceinline__ void settle() {
     __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
@@ -315,7 +321,7 @@ __global__ __launch_bounds__(kLpThreads, TOP ? 6 : 8) void logprobs_kernel(Logpr
 
   LpSums x{-__builtin_inff(), 0.f, 0.f, 0.f};  // (the same for all lanes)
   float s[kLpLoads] = {}, t[kLpLoads] = {};
-  [[maybe_unused]] LpPicked picked{room[TOP ? wave : 0], 0, 0, -__builtin_inff()};
+  [[maybe_unused]] LpPicked picked{room[TOP ? wave : 0], 0, 0, -__builtin_inff(), -__builtin_inff()};
   bool none = false;  // something is no number
   int q0 = from + wave * kLpWaveBlocks;
   const int q_first = q0;
@@ -386,16 +392,23 @@ __global__ __launch_bounds__(kLpThreads, TOP ? 6 : 8) void logprobs_kernel(Logpr
                                            });
         picked.raise((lp_key_t)all << 32);
       }
-      if (__ballot(!(top < picked.least)) != 0) {
+      const int token0 = q0 * EPV - lead;  // (the first row's may be negative: then all tokens are in question)
+      if (__ballot(!(top < picked.limit(max(token0, 0)))) != 0) {
         picked.raise(*(volatile lp_key_t*)&bound);
         const lp_key_t before = picked.floor;
+        // many lanes: the floor rises to what `top` of their maxima reach
+        if (__builtin_popcountll(__ballot(!(top < picked.limit(max(token0, 0))))) > min(max(p.top, 16), 48)) {
+          const uint32_t mine = spec_key(top);
+          picked.raise((lp_key_t)lp_search(lp_wave_max(mine), p.top, 2, [&](uint32_t at) { return __builtin_popcountll(__ballot(mine >= at)); }) << 32);
+        }
+        const float limit = picked.limit(max(token0, 0));
         // the blocks whose maximum passes go to LDS side by side, of all loads or, where they are many, of one
         bool pass[kLpLoads];
         uint64_t found[kLpLoads];
         int blocks_found = 0;
 #pragma unroll
         for (int j = 0; j < kLpLoads; ++j) {
-          pass[j] = !(lp_float(most[j], T{}) < picked.least);
+          pass[j] = !(lp_float(most[j], T{}) < limit);
           found[j] = __ballot(pass[j]);
           blocks_found += __builtin_popcountll(found[j]);
         }
@@ -493,7 +506,7 @@ __global__ __launch_bounds__(kLpThreads, TOP ? 6 : 8) void logprobs_kernel(Logpr
         for (int k = 0; k < AHEAD; ++k) key[k] = get(parts + min(i0 + k * kLpWaves, p.split - 1) * slot + 2 + lane);
       };
       ask(wave);
-      picked = LpPicked{room[wave], 0, 0, -__builtin_inff()};
+      picked = LpPicked{room[wave], 0, 0, -__builtin_inff(), -__builtin_inff()};
       picked.raise((lp_key_t)lp_wave_min((uint32_t)(qth >> 32)) << 32);
       for (int i0 = wave; i0 < p.split; i0 += AHEAD * kLpWaves) {
         if (i0 != wave) ask(i0);

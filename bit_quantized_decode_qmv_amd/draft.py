@@ -141,6 +141,7 @@ def logprobs(logits, tokens=None, top: int = 0, entropy: bool = False, workspace
     dtype = _bq.DTYPE_F16 if logits.dtype is torch.float16 else _bq.DTYPE_F32
     count, logprob, entropies, top_tokens, top_logprobs = 0, None, None, None, None
     if tokens is not None:
+        _gpu(tokens, "tokens")
         if tokens.dim() not in (1, 2):
             raise ValueError(f"tokens have shape {tuple(tokens.shape)}, expected [{rows}] or [{rows}][count]")
         count = 1 if tokens.dim() == 1 else tokens.shape[1]

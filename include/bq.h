@@ -78,7 +78,8 @@ typedef enum bq_status {
   BQ_ERR_M = -5,          /* M outside the range this entry point accepts */
   BQ_ERR_ALIGN = -6,      /* a pointer is misaligned, or a t5 repack with K % 256 != 0 */
   BQ_ERR_HIP = -7,        /* the HIP runtime rejected a launch */
-  BQ_ERR_FLAGS = -8,      /* bq_linear, bq_rope, bq_kv_append, bq_kv_attn: flags holds
+  BQ_ERR_FLAGS = -8,      /* bq_linear, bq_rope, bq_norm_rope, bq_kv_append,
+                             bq_kv_append_norm, bq_kv_attn: flags holds
                              undefined bits (or a window without BQ_KV_CAUSAL) */
   BQ_ERR_WORKSPACE = -9,  /* bq_spec_decode_verify, bq_kv_fork / resize / compact:
                              workspace NULL or too small */
@@ -551,8 +552,9 @@ int bq_kv_attn_tree(const bq_kv_cache* cache, int layer, const void* q, void* ou
  * largest of its own scale and its tokens' scales; its codes are brought to it
  * (rne; unchanged when the scale did not grow), so every token that no other
  * replaces keeps its value.  lens still counts all n rows.  A sequence whose
- * path does not rise from row to row inside 0 .. n - 1 is left as it is; a row
- * whose page is missing is not moved.  Pages that are written must not be
+ * path does not rise from row to row inside 0 .. n - 1, or that holds fewer
+ * tokens than rows, is left as it is; a row whose page, or whose place's, is
+ * missing is not moved.  Pages that are written must not be
  * shared (as for bq_kv_append). */
 int bq_tree_plan(const int* parent, const int* cu, const int* lens, int batch, int total, int mask_words, int window,
                  void* mask, int* pos, void* stream);
@@ -579,9 +581,11 @@ int bq_kv_keep(const bq_kv_cache* cache, const int* cu, const int* lens, const i
  * BQ_LOGPROBS_MAX_TOP, 0 <= rows < 2^24, 1 <= V < 2^28.
  * workspace: as bq_kv_attn's (its first BQ_LOGPROBS_COUNTER_BYTES zero before
  * the first use, zero again after every call; 16-byte aligned, NULL allowed):
- * it lets several workgroups share a row; less than bq_logprobs_workspace
- * gives says gives fewer of them.  Results may differ in the last bits by the
- * split, and are the same on every call with the same arguments. */
+ * it lets several workgroups share a row, bq_logprobs_workspace gives the size
+ * for as many as the library would take, less gives fewer.  Calls that overlap
+ * in time must not share one; one that serves bq_kv_attn serves here too.
+ * Results may differ in the last bits by the number of workgroups, and are the
+ * same on every call with the same arguments.  One launch. */
 #define BQ_LOGPROBS_MAX_TOP 64
 #define BQ_LOGPROBS_MAX_COUNT 1024
 #define BQ_LOGPROBS_COUNTER_BYTES 65536

@@ -102,6 +102,23 @@ def test_rising_and_falling_rows(dtype):
     run(np.stack([up_, up_[::-1], saw, -saw]), [[0, 59999, 30000]] * 4, top=64)
 
 
+@pytest.mark.parametrize("top", [1, 30, 64])
+def test_floors_between_equal_values(top):
+    """Few values over a long row, the largest of them rare, at its ends, in the middle: which of the equal ones are
+    among the largest is decided by tokens that other waves and parts hold."""
+    rng = np.random.default_rng(10)
+    for n in (3, 40, 200):
+        x = rng.integers(0, 2, (6, 90000)).astype(np.float16)
+        x[0, -n:] = 5
+        x[1, :n] = 5
+        x[2, 45000 - n:45000 + n] = 5
+        x[3, rng.integers(0, 90000, n)] = 5
+        x[4, ::max(1, 90000 // n)] = 5
+        x[5, 8192 * np.arange(1, 10)] = 5
+        for rows in (x, x[:, 1:], x[:, :20000].copy()):
+            run(np.ascontiguousarray(rows), top=top)
+
+
 @pytest.mark.parametrize("dtype", [np.float16, np.float32])
 def test_masked_infinite_and_missing_values(dtype):
     rng = np.random.default_rng(2)
@@ -240,7 +257,7 @@ def test_empty_and_refusals():
     lp, ent, tt, tl = bq.logprobs(x[:0], t[:0], 3, True)
     assert lp.shape == (0,) and ent.shape == (0,) and tt.shape == tl.shape == (0, 3)
     for bad in (dict(logits=x.double()), dict(logits=x[0]), dict(logits=x.t()), dict(logits=x[:, ::2]), dict(logits=x[:1].expand(2, 9)),
-                dict(tokens=t.long()), dict(tokens=t[:1]), dict(tokens=t[None, None]), dict(tokens=t.cpu()), dict(top=65), dict(top=-1),
+                dict(tokens=t.long()), dict(tokens=t[:1]), dict(tokens=t[None, None]), dict(tokens=t.cpu()), dict(tokens=[1, 2]), dict(top=65), dict(top=-1),
                 dict(tokens=None, top=0, entropy=False), dict(workspace=x), dict(logits=x[:, :0])):
         with pytest.raises((ValueError, TypeError, bq.BQError)):
             bq.logprobs(**{**dict(logits=x, tokens=t, top=2, entropy=True), **bad})

@@ -109,6 +109,17 @@ def test_accept_ignores_rows_past_the_limit_and_parents_that_are_none():
     assert path[0].tolist() == [0, 4, -1, -1] and nxt[0] == 7
 
 
+def test_no_rows_at_all():
+    import bit_quantized_decode_qmv_amd as bq
+    torch = torch_mod()
+    none = torch.empty(0, dtype=torch.int32, device="cuda:0")
+    cu, lens = up([0, 0, 0], np.int32), up([5, 0], np.int32)
+    mask, pos = bq.tree_plan(none, cu, lens, words=2)
+    assert mask.shape == (0, 2) and pos.shape == (0,)
+    path, kept, nxt, want = bq.tree_accept(none, none, none, cu, lens, 3)
+    assert path.tolist() == [[-1] * 3] * 2 and kept.tolist() == [0, 0] and nxt.tolist() == [-1, -1] and want.tolist() == [5, 0]
+
+
 def keep(c, table, lens, news, paths, kept=None, most=None):
     import bit_quantized_decode_qmv_amd as bq
     most = most or max(max(map(len, paths)), 1)
