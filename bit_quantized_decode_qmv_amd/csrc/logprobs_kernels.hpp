@@ -17,15 +17,16 @@
 // compares its maximum, which the softmax needs anyway, and only where one
 // passes are the values of its 16-byte blocks that pass looked at, side by side,
 // a thread one (through LDS: a register has no number that a thread could
-// choose).  The floor begins at what
-// the maxima of a workgroup's first 1024 blocks say (`top` lanes hold a value
-// from it on, so as many values are), rises by a wave's maxima where most of
-// its lanes pass, and when the room runs out: then the `top` largest are found
-// by bisection, a count over the wave for each step, and the others leave.  A
-// value equal to the floor's passes only with a lower token.  In the end the waves' and the parts' numbers are
-// put together the same way, and each of the `top` finds its place by counting
-// those above it.  So ties and order change nothing but the time, and that by a
-// bounded factor.
+// choose).  The floor begins at what the maxima of a workgroup's first 1024
+// blocks say (`top` lanes hold a value from it on, so as many values are), rises
+// by a wave's maxima where most of its lanes pass, and when the room runs out:
+// then the `top` largest are found by bisection, a count over the wave for each
+// step, and the others leave.  A value equal to the floor's passes only with a
+// lower token.  In the end the waves' and the parts' numbers are put together
+// the same way, and each of the `top` finds its place by counting those above
+// it.  So ties and order change nothing but the time: 2047 rows of 151936 in
+// fp16, top 1, 20 and 64, take 125, 136 and 140 us with random values, 118, 119
+// and 119 with equal ones, 137, 275 and 859 with values that rise all along.
 #pragma once
 
 #include "kv_common.hpp"
@@ -296,9 +297,16 @@ __device__ __forceinline__ LpSums lp_join(LpSums x) {
 
 // One workgroup for a part of a row (of the whole row where rows fill the
 // chip); a row's parts are joined by the one that finishes last.  A wave takes
-// 4 KB at a time; what hides its loads is the other waves of its SIMD.  Bound by HBM
-// where rows are many, then by issue: of a value two conversions and sums, an
-// exponential and a share of the maxima.  Measured: MEASURED_LP.
+// 4 KB at a time; what hides its loads is the other waves of its SIMD.  Many rows
+// are bound by HBM and, not far behind, by issue (a conversion, a product, an
+// exponential and two sums for a value), few by the chain of latencies from the
+// first load to the join.  Measured with entropy, us without alternatives and
+// with 1, 5, 20 and 64: 2047 rows of 151936 in fp16 110, 121, 127, 133 and 141
+// (622 MB: 5.7 to 4.4 TB/s), 301 rows of it 20.6, 27.6, 31.8, 35.6 and 47.4, 5
+// rows 5.6, 9.7, 11.5, 13.9 and 19.4; 301 rows of 32000 in fp32 11.1, 15.7, 17.2,
+// 19.2 and 24.6.  Eight waves a SIMD with alternatives, which take some registers
+// to memory: 123, 128, 132 and 136 us for the first of these, 28.3, 32.8, 37.4 and
+// 49.6 for the second.
 template <typename T, bool ENTROPY, bool TOP>
 __global__ __launch_bounds__(kLpThreads, TOP ? 6 : 8) void logprobs_kernel(LogprobsParams p) {
   constexpr int EPV = 16 / (int)sizeof(T);  // values of a 16-byte block
@@ -381,22 +389,20 @@ __global__ __launch_bounds__(kLpThreads, TOP ? 6 : 8) void logprobs_kernel(Logpr
         uint32_t of[kLpWaves], largest = 0;
 #pragma unroll
         for (int i = 0; i < kLpWaves; ++i) largest = max(largest, of[i] = first[64 * i + lane]);
-        // (few are found as well among the largest of four lanes each)
-        const uint32_t most_of = lp_wave_max(largest);
-        const uint32_t all = p.top <= 24 ? lp_search(most_of, p.top, 2, [&](uint32_t at) { return __builtin_popcountll(__ballot(largest >= at)); })
-                                         : lp_search(most_of, p.top, 2, [&](uint32_t at) {
-                                             int reach = 0;
+        picked.raise((lp_key_t)lp_search(lp_wave_max(largest), p.top, 2, [&](uint32_t at) {
+          int reach = 0;
 #pragma unroll
-                                             for (int i = 0; i < kLpWaves; ++i) reach += __builtin_popcountll(__ballot(of[i] >= at));
-                                             return reach;
-                                           });
-        picked.raise((lp_key_t)all << 32);
+          for (int i = 0; i < kLpWaves; ++i) reach += __builtin_popcountll(__ballot(of[i] >= at));
+          return reach;
+        }) << 32);
       }
       const int token0 = q0 * EPV - lead;  // (the first row's may be negative: then all tokens are in question)
       if (__ballot(!(top < picked.limit(max(token0, 0)))) != 0) {
         picked.raise(*(volatile lp_key_t*)&bound);
         const lp_key_t before = picked.floor;
         // many lanes: the floor rises to what `top` of their maxima reach
+        // (without this, 2047 rows of values that rise took 1111 us for the
+        // largest and 2423 for 64)
         if (__builtin_popcountll(__ballot(!(top < picked.limit(max(token0, 0))))) > min(max(p.top, 16), 48)) {
           const uint32_t mine = spec_key(top);
           picked.raise((lp_key_t)lp_search(lp_wave_max(mine), p.top, 2, [&](uint32_t at) { return __builtin_popcountll(__ballot(mine >= at)); }) << 32);
