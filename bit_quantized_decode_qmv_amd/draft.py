@@ -90,7 +90,7 @@ def tree_plan(parent, cu, lens, words: int = 1, window: int = 0):
     if not 1 <= words <= _kv.TREE_MAX_WORDS:
         raise ValueError(f"words = {words}, expected 1 .. {_kv.TREE_MAX_WORDS}")
     mask = torch.empty((total, words), dtype=torch.int64, device=dev)
-    pos = torch.empty(total, dtype=torch.int32, device=dev)
+    pos = torch.empty_like(parent)
     _kv._launch(dev, "bq_tree_plan", parent.data_ptr(), cu.data_ptr(), lens.data_ptr(), batch, total, words,
                 _kv._window(window, "window"), mask.data_ptr(), pos.data_ptr())
     return mask, pos
@@ -104,13 +104,12 @@ def tree_accept(target, token, parent, cu, lens, max_path: int):
     target, token, parent: int32 [total], target[row] the token that the target
     model has after the row, token[row] the row's own."""
     dev, batch, total = _sequences(parent, cu, lens)
-    torch = _kv._torch
     _ints(target, "target", dev, total)
     _ints(token, "token", dev, total)
     if not 1 <= max_path <= _kv.TREE_MAX_ROWS:
         raise ValueError(f"max_path = {max_path}, expected 1 .. {_kv.TREE_MAX_ROWS}")
-    path = torch.empty((batch, max_path), dtype=torch.int32, device=dev)
-    told = torch.empty((3, batch), dtype=torch.int32, device=dev)
+    path = parent.new_empty((batch, max_path))
+    told = parent.new_empty((3, batch))
     at = told.data_ptr()
     _kv._launch(dev, "bq_tree_accept", target.data_ptr(), token.data_ptr(), parent.data_ptr(), cu.data_ptr(),
                 lens.data_ptr(), batch, total, max_path, path.data_ptr(), at, at + 4 * batch, at + 8 * batch)

@@ -374,7 +374,8 @@ def kv_read(cache: KVCache, layer: int, cu, lens, table, total: int):
     dev = cache.device
     batch, max_pages = _batch(cu, lens, table, dev)
     _int(total, "total")
-    k, v = (_torch.empty((total, cache.kv_heads, cache.head_dim), dtype=_torch.float16, device=dev) for _ in range(2))
+    k = _torch.empty((total, cache.kv_heads, cache.head_dim), dtype=_torch.float16, device=dev)
+    v = _torch.empty_like(k)
     _launch(dev, "bq_kv_read", cache.desc, _int(layer, "layer"), k.data_ptr(), v.data_ptr(), cu.data_ptr(), lens.data_ptr(),
             table.data_ptr(), batch, max_pages, total)
     return k, v
