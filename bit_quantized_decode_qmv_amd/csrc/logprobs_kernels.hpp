@@ -19,14 +19,15 @@
 // a thread one (through LDS: a register has no number that a thread could
 // choose).  The floor begins at what the maxima of a workgroup's first 1024
 // blocks say (`top` lanes hold a value from it on, so as many values are), rises
-// by a wave's maxima where most of its lanes pass, and when the room runs out:
-// then the `top` largest are found by bisection, a count over the wave for each
-// step, and the others leave.  A value equal to the floor's passes only with a
-// lower token.  In the end the waves' and the parts' numbers are put together
-// the same way, and each of the `top` finds its place by counting those above
-// it.  So ties and order change nothing but the time: 2047 rows of 151936 in
-// fp16, top 1, 20 and 64, take 125, 136 and 140 us with random values, 118, 119
-// and 119 with equal ones, 137, 275 and 859 with values that rise all along.
+// with the lanes' maxima over more of them, by a wave's maxima where most of its
+// lanes pass, and when the room runs out: then the `top` largest are found by
+// bisection, a count over the wave for each step, and the others leave.  A value
+// equal to the floor's passes only with a lower token.  In the end the waves' and
+// the parts' numbers are put together the same way, and each of the `top` finds
+// its place by counting those above it.  So ties and order change nothing but the
+// time: 2047 rows of 151936 in fp16, top 1, 20 and 64, take 122, 131 and 139 us
+// with random values, 123, 124 and 125 with equal ones, 138, 278 and 846 with
+// values that rise all along.
 #pragma once
 
 #include "kv_common.hpp"
@@ -301,12 +302,13 @@ __device__ __forceinline__ LpSums lp_join(LpSums x) {
 // are bound by HBM and, not far behind, by issue (a conversion, a product, an
 // exponential and two sums for a value), few by the chain of latencies from the
 // first load to the join.  Measured with entropy, us without alternatives and
-// with 1, 5, 20 and 64: 2047 rows of 151936 in fp16 110, 121, 127, 133 and 141
-// (622 MB: 5.7 to 4.4 TB/s), 301 rows of it 20.6, 27.6, 31.8, 35.6 and 47.4, 5
-// rows 5.6, 9.7, 11.5, 13.9 and 19.4; 301 rows of 32000 in fp32 11.1, 15.7, 17.2,
-// 19.2 and 24.6.  Eight waves a SIMD with alternatives, which take some registers
-// to memory: 123, 128, 132 and 136 us for the first of these, 28.3, 32.8, 37.4 and
-// 49.6 for the second.
+// with 1, 5, 20 and 64: 2047 rows of 151936 in fp16 110, 118, 122, 128 and 140
+// (622 MB: 5.7 to 4.4 TB/s), 301 rows of it 20.6, 28.0, 32.0, 36.6 and 48, 5
+// rows 5.6, 9.9, 11.4, 14.0 and 18.6; 301 rows of 32000 in fp32 11.1, 15.8, 17.9,
+// 20.0 and 24.8.  Seven waves a SIMD with alternatives, which take some registers
+// to memory and leave fewer workgroups a last round of their own: 129, 134, 140
+// and 149 us for the first of these, 29.1, 33.2, 37.6 and 49.1 for the second; five
+// 116, 119, 127 and 141, but 2047 rows of 32000 37.3 for 35.7 (top 5).
 template <typename T, bool ENTROPY, bool TOP>
 __global__ __launch_bounds__(kLpThreads, TOP ? 6 : 8) void logprobs_kernel(LogprobsParams p) {
   constexpr int EPV = 16 / (int)sizeof(T);  // values of a 16-byte block
@@ -330,6 +332,8 @@ __global__ __launch_bounds__(kLpThreads, TOP ? 6 : 8) void logprobs_kernel(Logpr
   LpSums x{-__builtin_inff(), 0.f, 0.f, 0.f};  // (the same for all lanes)
   float s[kLpLoads] = {}, t[kLpLoads] = {};
   [[maybe_unused]] LpPicked picked{room[TOP ? wave : 0], 0, 0, -__builtin_inff(), -__builtin_inff()};
+  [[maybe_unused]] float seen = -__builtin_inff();  // the largest that the lane has met
+  [[maybe_unused]] int pass = 0;
   bool none = false;  // something is no number
   int q0 = from + wave * kLpWaveBlocks;
   const int q_first = q0;
@@ -381,11 +385,21 @@ __global__ __launch_bounds__(kLpThreads, TOP ? 6 : 8) void logprobs_kernel(Logpr
         if constexpr (ENTROPY) t[j] = __builtin_fmaf(y, f, t[j]);
       }
     if constexpr (TOP) {
-      if (q0 == q_first) {
-        // `top` of the workgroup's lanes hold a value that reaches the floor
-        first[threadIdx.x] = q0 < to ? spec_key(top) : 0u;
-        if (threadIdx.x == 0) bound = 0;
-        __syncthreads();
+      // `top` of the workgroup's lanes have met a value that reaches the floor;
+      // found anew after 4, 8, .. passes, if some are left, then without waiting
+      // for the others, of whom an older maximum is as true (2047 rows of 151936,
+      // top 5, 127 -> 122 us; after the second pass too, 2047 rows of 32000 take
+      // 39 for 36)
+      seen = __builtin_fmaxf(seen, top);
+      ++pass;
+      if (pass == 1 || (pass >= 4 && (pass & (pass - 1)) == 0 && q0 + 4 * kLpBlocks < to)) {
+        first[threadIdx.x] = q0 < to ? spec_key(seen) : 0u;
+        if (pass == 1) {
+          if (threadIdx.x == 0) bound = 0;
+          __syncthreads();
+        } else {
+          LpPicked::settle();
+        }
         uint32_t of[kLpWaves], largest = 0;
 #pragma unroll
         for (int i = 0; i < kLpWaves; ++i) largest = max(largest, of[i] = first[64 * i + lane]);
