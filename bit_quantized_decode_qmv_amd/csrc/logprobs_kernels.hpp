@@ -25,8 +25,8 @@
 // equal to the floor's passes only with a lower token.  In the end the waves' and
 // the parts' numbers are put together the same way, and each of the `top` finds
 // its place by counting those above it.  So ties and order change nothing but the
-// time: 2047 rows of 151936 in fp16, top 1, 20 and 64, take 122, 131 and 139 us
-// with random values, 123, 124 and 125 with equal ones, 138, 278 and 846 with
+// time: 2047 rows of 151936 in fp16, top 1, 20 and 64, take 122, 129 and 137 us
+// with random values, 120, 120 and 121 with equal ones, 139, 278 and 846 with
 // values that rise all along.
 #pragma once
 
@@ -302,13 +302,12 @@ __device__ __forceinline__ LpSums lp_join(LpSums x) {
 // are bound by HBM and, not far behind, by issue (a conversion, a product, an
 // exponential and two sums for a value), few by the chain of latencies from the
 // first load to the join.  Measured with entropy, us without alternatives and
-// with 1, 5, 20 and 64: 2047 rows of 151936 in fp16 110, 118, 122, 128 and 140
-// (622 MB: 5.7 to 4.4 TB/s), 301 rows of it 20.6, 28.0, 32.0, 36.6 and 48, 5
-// rows 5.6, 9.9, 11.4, 14.0 and 18.6; 301 rows of 32000 in fp32 11.1, 15.8, 17.9,
-// 20.0 and 24.8.  Seven waves a SIMD with alternatives, which take some registers
-// to memory and leave fewer workgroups a last round of their own: 129, 134, 140
-// and 149 us for the first of these, 29.1, 33.2, 37.6 and 49.1 for the second; five
-// 116, 119, 127 and 141, but 2047 rows of 32000 37.3 for 35.7 (top 5).
+// with 1, 5, 20 and 64: 2047 rows of 151936 in fp16 110, 118, 121, 128 and 140
+// (622 MB: 5.7 to 4.4 TB/s), 301 rows of it 20.6, 28.1, 32.0, 36.2 and 47.4, 5
+// rows 5.6, 9.7, 11.4, 13.9 and 19.5; 301 rows of 32000 in fp32 11.1, 15.8, 17.7,
+// 19.9 and 24.8.  Eight waves a SIMD with alternatives, which take some registers
+// to memory: 123, 126, 129 and 136 us for the first of these, 29.4, 33.6, 38.5 and
+// 50.4 for the second; five waves 115, 119, 126 and 142, 28.4, 32.8, 36.4 and 47.9.
 template <typename T, bool ENTROPY, bool TOP>
 __global__ __launch_bounds__(kLpThreads, TOP ? 6 : 8) void logprobs_kernel(LogprobsParams p) {
   constexpr int EPV = 16 / (int)sizeof(T);  // values of a 16-byte block
