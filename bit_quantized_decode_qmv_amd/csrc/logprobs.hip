@@ -24,8 +24,8 @@ int check_sizes(int rows, int V, int logits_dtype, int top) {
 // Workgroups of a row, and the passes of each: as many as bring the call to
 // kTarget workgroups, no more than a row has passes (a value may start
 // anywhere in a 16-byte block) or `room` holds.  Measured, us with 512, 1024 and
-// 2048: 301 rows of 151936 in fp16, top 5, 35.8, 31.8 and 31.4, 700 rows of 50000
-// 24.0, 23.6 and 29.4 (a part costs its first pass's barrier, its list and its
+// 2048: 301 rows of 151936 in fp16, top 5, 33.4, 30.6 and 30.8, 700 rows of 50000
+// 23.4, 23.5 and 29.1 (a part costs its first pass's barrier, its list and its
 // share of the join); 5 rows of 151936 and 301 of 32000 in fp32 alike.
 constexpr int kTarget = 1024;
 struct Split {

@@ -22,12 +22,11 @@
 // with the lanes' maxima over more of them, by a wave's maxima where most of its
 // lanes pass, and when the room runs out: then the `top` largest are found by
 // bisection, a count over the wave for each step, and the others leave.  A value
-// equal to the floor's passes only with a lower token.  In the end the waves' and
-// the parts' numbers are put together the same way, and each of the `top` finds
-// its place by counting those above it.  So ties and order change nothing but the
-// time: 2047 rows of 151936 in fp16, top 1, 20 and 64, take 122, 129 and 137 us
-// with random values, 120, 120 and 121 with equal ones, 139, 278 and 846 with
-// values that rise all along.
+// equal to the floor's passes only with a lower token.  In the end each of the
+// waves' numbers, then of the parts', finds its place by counting those above it.
+// So ties and order change nothing but the time: 2047 rows of 151936 in fp16, top
+// 1, 20 and 64, take 122, 131 and 139 us with random values, 121, 122 and 127 with
+// equal ones, 144, 280 and 843 with values that rise all along.
 #pragma once
 
 #include "kv_common.hpp"
@@ -42,7 +41,8 @@ constexpr int kLpBlocks = kLpWaves * kLpWaveBlocks;      // and a workgroup
 constexpr int kLpMaxSplit = 64;
 constexpr int kLpCounterStride = 8;                      // 4-byte words between rows
 constexpr int kLpSplitRows = BQ_LOGPROBS_COUNTER_BYTES / (4 * kLpCounterStride);
-constexpr int kLpRoom = 256;                             // numbers a wave collects
+constexpr int kLpAhead = 3;                              // parts a wave asks for at a time
+constexpr int kLpRoom = 64 * (1 + kLpAhead);             // numbers a wave collects
 constexpr int kLpStage = 64;                             // blocks whose values it looks at
 
 struct LogprobsParams {
@@ -61,6 +61,7 @@ struct LogprobsParams {
 constexpr int lp_slot(int top) { return top > 0 ? 2 + 64 : 2; }
 
 typedef unsigned long long lp_key_t;
+typedef lp_key_t lp_pair_t __attribute__((ext_vector_type(2)));
 
 // The largest t found that at least `want` of some numbers reach (0 where fewer
 // reach 0), by distances below the largest of them: first powers of two, then
@@ -151,34 +152,25 @@ struct LpPicked {
     __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
     __builtin_amdgcn_wave_barrier();
   }
-  // The lanes' numbers from the floor on join (0: none).
-  __device__ __forceinline__ void add(lp_key_t key, int top) {
-    uint64_t found = __ballot(key != 0 && key >= floor);
-    if (found == 0) return;
-    if (n > kLpRoom - 64) {
-      keep(top);
-      found = __ballot(key != 0 && key >= floor);
-    }
+  __device__ __forceinline__ uint64_t found(lp_key_t key) const { return __ballot(key != 0 && key >= floor); }  // (0: none)
+  // The lanes' numbers from the floor on join; there is room for them.
+  __device__ __forceinline__ void add(lp_key_t key) {
+    const uint64_t in = found(key);
     if (key != 0 && key >= floor)
-      room[n + __builtin_amdgcn_mbcnt_hi((uint32_t)(found >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)found, 0))] = key;
-    n += __builtin_popcountll(found);
+      room[n + __builtin_amdgcn_mbcnt_hi((uint32_t)(in >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)in, 0))] = key;
+    n += __builtin_popcountll(in);
   }
-  // How many are larger than the lane's own (of at most 64).
-  __device__ __forceinline__ int place(lp_key_t key) const {
-    int above = 0;
-#pragma unroll 8
-    for (int i = 0; i < n; ++i) above += room[i] > key;  // (the same for all lanes: one read)
-    return above;
+  // Their number, for others, who read them in twos.
+  __device__ __forceinline__ void end(int& count) const {
+    if ((threadIdx.x & 63) != 0) return;
+    count = n;
+    if (n & 1) room[n] = 0;
   }
   // All but the `top` largest leave.
   __device__ __forceinline__ void keep(int top) {
+    constexpr int EACH = kLpRoom / 64;
     settle();
     if (n <= top) return;
-    if (n <= 64) keep<1>(top);
-    else keep<kLpRoom / 64>(top);
-  }
-  template <int EACH>
-  __device__ __forceinline__ void keep(int top) {
     lp_key_t key[EACH];
 #pragma unroll
     for (int i = 0; i < EACH; ++i) {
@@ -302,16 +294,21 @@ __device__ __forceinline__ LpSums lp_join(LpSums x) {
 // are bound by HBM and, not far behind, by issue (a conversion, a product, an
 // exponential and two sums for a value), few by the chain of latencies from the
 // first load to the join.  Measured with entropy, us without alternatives and
-// with 1, 5, 20 and 64: 2047 rows of 151936 in fp16 110, 118, 121, 128 and 140
-// (622 MB: 5.7 to 4.4 TB/s), 301 rows of it 20.6, 28.1, 32.0, 36.2 and 47.4, 5
-// rows 5.6, 9.7, 11.4, 13.9 and 19.5; 301 rows of 32000 in fp32 11.1, 15.8, 17.7,
-// 19.9 and 24.8.  Eight waves a SIMD with alternatives, which take some registers
-// to memory: 123, 126, 129 and 136 us for the first of these, 29.4, 33.6, 38.5 and
-// 50.4 for the second; five waves 115, 119, 126 and 142, 28.4, 32.8, 36.4 and 47.9.
+// with 1, 5, 20 and 64: 2047 rows of 151936 in fp16 111, 118, 122, 127 and 140
+// (622 MB: 5.6 to 4.4 TB/s), 301 rows of it 20.7, 27.1, 30.6, 34.7 and 45.4, 5
+// rows 5.3, 9.8, 10.8, 12.0 and 14.3; 301 rows of 32000 in fp32 11.1, 14.8, 16.7,
+// 18.4 and 24.5.  Eight waves a SIMD with alternatives, which take some registers
+// to memory: 127, 130, 133 and 142 us for the first of these, 30.3, 33.2, 37.8 and
+// 48.9 for the second; five waves 115, 119, 124 and 139, but 2047 rows of 32000
+// take 36.2 for 34.6 (top 5).  The next pass's loads asked for a pass ahead: 132
+// us (top 5, 16 registers more).  Numbers are ranked by a thread each, and the
+// finding of the `top` largest by bisection stands in three places only: with
+// one wave that put them together first, and eight places, the code was 45 KB
+// for 25, and 5 rows took 13.5 and 19.0 us (top 20 and 64).
 template <typename T, bool ENTROPY, bool TOP>
 __global__ __launch_bounds__(kLpThreads, TOP ? 6 : 8) void logprobs_kernel(LogprobsParams p) {
   constexpr int EPV = 16 / (int)sizeof(T);  // values of a 16-byte block
-  __shared__ lp_key_t room[TOP ? kLpWaves : 1][TOP ? kLpRoom : 1];
+  __shared__ __align__(16) lp_key_t room[TOP ? kLpWaves : 1][TOP ? kLpRoom : 1];
   __shared__ __align__(16) u32x4_t stage[TOP ? kLpWaves : 1][TOP ? kLpStage : 1];
   __shared__ short stage_of[TOP ? kLpWaves : 1][TOP ? kLpStage : 1];
   __shared__ lp_key_t bound;        // the highest of the waves' floors
@@ -450,7 +447,10 @@ __global__ __launch_bounds__(kLpThreads, TOP ? 6 : 8) void logprobs_kernel(Logpr
             const int at = min(i, n - 1), q = q0 + stage_of[TOP ? wave : 0][at];
             const T value = reinterpret_cast<const T*>(&stage[TOP ? wave : 0][at])[lane % EPV];
             const int64_t v = (int64_t)q * EPV + lane % EPV - lead;
-            picked.add(i < n && q < to && v >= 0 && v < p.V ? spec_pack(spec_key((float)value), (int)v) : 0ull, p.top);
+            const lp_key_t key = i < n && q < to && v >= 0 && v < p.V ? spec_pack(spec_key((float)value), (int)v) : 0ull;
+            if (picked.found(key) == 0) continue;
+            if (picked.n > kLpRoom - 64) picked.keep(p.top);
+            picked.add(key);
           }
           LpPicked::settle();
         }
@@ -463,26 +463,51 @@ __global__ __launch_bounds__(kLpThreads, TOP ? 6 : 8) void logprobs_kernel(Logpr
   if constexpr (ENTROPY) x.t = lp_wave_sum((t[0] + t[1]) + (t[2] + t[3]));
   if (__ballot(none) != 0) x.m = __builtin_nanf("");
   if (lane == 0) sums[wave] = x;
-  // wave 0 takes what the others collected, and leaves `most` of them
-  const auto gather = [&]([[maybe_unused]] int most) {
+  // A round for the part, and, where a row has several, one for the row.
+  LpSums own;  // of the lane's wave, then of its part
+  [[maybe_unused]] lp_key_t key;  // of the thread, of the n numbers that the waves collected
+  [[maybe_unused]] int n, above;  // and how many of those are larger
+  for (int round = 1;; ++round) {
     if constexpr (TOP) {
-      if (lane == 0) counts[wave] = picked.n;
+      picked.end(counts[wave]);
     }
     __syncthreads();
     if constexpr (TOP) {
-      if (wave == 0) {
-        for (int i = 1; i < kLpWaves; ++i) {
-          const int n = __builtin_amdgcn_readfirstlane(counts[i]);
-          for (int at = 0; at < n; at += 64) picked.add(at + lane < n ? room[i][at + lane] : 0ull, p.top);
-        }
-        if (picked.n > most) picked.keep(p.top);
+      int of[kLpWaves];
+      const auto count = [&] {
+        n = 0;
+#pragma unroll
+        for (int i = 0; i < kLpWaves; ++i) n += of[i] = __builtin_amdgcn_readfirstlane(counts[i]);
+      };
+      count();
+      if (n > kLpThreads) {
+        __syncthreads();
+        if (picked.n > 64) picked.keep(p.top);  // (64 at most)
+        picked.end(counts[wave]);
+        __syncthreads();
+        count();
       }
+      int at = (int)threadIdx.x;
+      key = 0;
+      above = 0;
+#pragma unroll
+      for (int i = 0; i < kLpWaves; ++i) {
+        if (at >= 0 && at < of[i]) key = room[i][at];
+        at -= of[i];
+      }
+      if (64 * wave < n)
+        for (int i = 0; i < kLpWaves; ++i) {
+          const int many = __builtin_amdgcn_readfirstlane(counts[i]);
+#pragma unroll 8
+          for (int k = 0; k < many; k += 2) {  // (the same for all lanes: one read)
+            const lp_pair_t two = *reinterpret_cast<const lp_pair_t*>(&room[i][k]);
+            above += (two[0] > key) + (two[1] > key);
+          }
+        }
     }
-  };
-  gather(p.split > 1 ? 64 : p.top);
-  const LpSums nothing{-__builtin_inff(), 0.f, 0.f, 0.f};
-  if (wave == 0) x = lp_join<T>(lane < kLpWaves ? sums[lane] : nothing);
-  if (p.split > 1) {
+    if (round == 1) own = lane < kLpWaves ? sums[lane] : LpSums{-__builtin_inff(), 0.f, 0.f, 0.f};
+    x = lp_join<T>(own);
+    if (round == 2 || p.split == 1) break;
     const int slot = lp_slot(p.top);
     uint64_t* mine = p.part + (int64_t)blockIdx.x * slot;
     const auto pack = [](float a, float b) {
@@ -493,21 +518,19 @@ __global__ __launch_bounds__(kLpThreads, TOP ? 6 : 8) void logprobs_kernel(Logpr
     };
     const auto get = [](const uint64_t* at) { return __hip_atomic_load(at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
     unsigned* counter = p.counters + row * kLpCounterStride;
-    if (wave == 0) {
-      if (lane == 0) {
-        put(mine, pack(x.m, x.b));
-        put(mine + 1, pack(x.s, x.t));
-      }
-      if constexpr (TOP) {
-        picked.settle();
-        const lp_key_t key = lane < picked.n ? room[0][lane] : 0ull;
-        put(mine + 2 + (key != 0 ? picked.place(key) : lane), key);
-      }
-      // the stores are performed at device scope before the count is
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      if (lane == 0)
-        last = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (unsigned)(p.split - 1);
+    if (threadIdx.x == 0) {
+      put(mine, pack(x.m, x.b));
+      put(mine + 1, pack(x.s, x.t));
     }
+    if constexpr (TOP) {
+      if (key != 0 && above < 64) put(mine + 2 + above, key);
+      if ((int)threadIdx.x >= n && threadIdx.x < 64) put(mine + 2 + threadIdx.x, 0ull);
+    }
+    // every wave's stores are performed at device scope before the count is
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (threadIdx.x == 0)
+      last = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (unsigned)(p.split - 1);
     __syncthreads();
     if (!last) return;
     // the row's parts, a lane each; their numbers, a wave every fourth
@@ -518,53 +541,47 @@ __global__ __launch_bounds__(kLpThreads, TOP ? 6 : 8) void logprobs_kernel(Logpr
       // Each part but the last has `top` numbers at least, so `top` reach the lowest of their q-th ones.
       const int q = (p.top + p.split - 2) / (p.split - 1);
       const uint64_t qth = get(parts + min(lane, p.split - 2) * slot + 2 + q - 1);
-      constexpr int AHEAD = 5;
-      lp_key_t key[AHEAD];
-      const auto ask = [&](int i0) {
-#pragma unroll
-        for (int k = 0; k < AHEAD; ++k) key[k] = get(parts + min(i0 + k * kLpWaves, p.split - 1) * slot + 2 + lane);
-      };
-      ask(wave);
+      lp_key_t ahead[kLpAhead];
       picked = LpPicked{room[wave], 0, 0, -__builtin_inff(), -__builtin_inff()};
-      picked.raise((lp_key_t)lp_wave_min((uint32_t)(qth >> 32)) << 32);
-      for (int i0 = wave; i0 < p.split; i0 += AHEAD * kLpWaves) {
-        if (i0 != wave) ask(i0);
+      for (int i0 = wave; i0 < p.split; i0 += kLpAhead * kLpWaves) {
 #pragma unroll
-        for (int k = 0; k < AHEAD; ++k) picked.add(i0 + k * kLpWaves < p.split ? key[k] : 0ull, p.top);
+        for (int k = 0; k < kLpAhead; ++k) ahead[k] = get(parts + min(i0 + k * kLpWaves, p.split - 1) * slot + 2 + lane);
+        if (i0 == wave) picked.raise((lp_key_t)lp_wave_min((uint32_t)(qth >> 32)) << 32);
+        int more = 0;
+#pragma unroll
+        for (int k = 0; k < kLpAhead; ++k) {
+          if (i0 + k * kLpWaves >= p.split) ahead[k] = 0;
+          more += __builtin_popcountll(picked.found(ahead[k]));
+        }
+        if (picked.n + more > kLpRoom) picked.keep(p.top);
+#pragma unroll
+        for (int k = 0; k < kLpAhead; ++k) picked.add(ahead[k]);
       }
     }
-    gather(p.top);
-    if (wave == 0) {
-      x = nothing;
-      if (lane < p.split) {
-        x.m = __builtin_bit_cast(float, (uint32_t)mb);
-        x.b = __builtin_bit_cast(float, (uint32_t)(mb >> 32));
-        x.s = __builtin_bit_cast(float, (uint32_t)st);
-        x.t = __builtin_bit_cast(float, (uint32_t)(st >> 32));
-      }
-      x = lp_join<T>(x);
+    own = LpSums{-__builtin_inff(), 0.f, 0.f, 0.f};
+    if (lane < p.split) {
+      own.m = __builtin_bit_cast(float, (uint32_t)mb);
+      own.b = __builtin_bit_cast(float, (uint32_t)(mb >> 32));
+      own.s = __builtin_bit_cast(float, (uint32_t)st);
+      own.t = __builtin_bit_cast(float, (uint32_t)(st >> 32));
     }
     if (threadIdx.x == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
-  if (wave == 0 && lane == 0) sums[0] = x;
-  __syncthreads();
-  x = sums[0];
   // a row without probabilities: something is no number, +inf, or all is -inf
   const float nan = __builtin_nanf("");
   const bool fine = x.m > -__builtin_inff() && x.m < __builtin_inff();
   const float log_s = logf(x.s), shift = fine ? log_s - lp_rounding(x.m, x.b, T{}) : nan;
   if (ENTROPY && threadIdx.x == 0) p.entropy[row] = fine ? log_s - kLn2 * (x.t / x.s) : nan;
   if constexpr (TOP) {
-    if (wave == 0) {
-      const lp_key_t key = lane < picked.n ? room[0][lane] : 0ull;
-      int place = picked.place(key);
-      if (lane < p.top) {
-        if (lane >= picked.n) place = lane;  // behind the vocabulary
-        const float value = __builtin_bit_cast(float, SpecBits<float>::value_of((uint32_t)(key >> 32)));
-        p.top_tokens[(int64_t)row * p.top + place] = key != 0 ? (int)(0xFFFFFFFFu - (uint32_t)key) : -1;
-        p.top_logprobs[(int64_t)row * p.top + place] = key != 0 ? (value - x.m) - shift : -__builtin_inff();
-      }
+    const auto tell = [&](int place, int token, float value) {
+      p.top_tokens[(int64_t)row * p.top + place] = token;
+      p.top_logprobs[(int64_t)row * p.top + place] = value;
+    };
+    if (key != 0 && above < p.top) {
+      const float value = __builtin_bit_cast(float, SpecBits<float>::value_of((uint32_t)(key >> 32)));
+      tell(above, (int)(0xFFFFFFFFu - (uint32_t)key), (value - x.m) - shift);
     }
+    if ((int)threadIdx.x >= n && (int)threadIdx.x < p.top) tell((int)threadIdx.x, -1, -__builtin_inff());  // behind the vocabulary
   }
   for (int i = (int)threadIdx.x; i < p.count; i += kLpThreads) {
     const int token = p.tokens[(int64_t)row * p.count + i];
