@@ -119,6 +119,25 @@ def test_floors_between_equal_values(top):
             run(np.ascontiguousarray(rows), top=top)
 
 
+@pytest.mark.parametrize("top", [1, 20, 64])
+@pytest.mark.parametrize("dtype", [np.float16, np.float32])
+def test_whole_rows_of_one_workgroup(dtype, top):
+    """Rows that no other workgroup shares: what has to pass rises along the row, from one pass over it to the next."""
+    import bit_quantized_decode_qmv_amd as bq
+    torch = torch_mod()
+    rng = np.random.default_rng(12)
+    V = 151 * 1024 + 3
+    x = (rng.standard_normal((8, V)) * 2.5).astype(dtype)
+    x[1] = np.linspace(-9, 9, V)
+    x[2] = x[1, ::-1]
+    x[3, -64:] += 20                                   # the largest at the end
+    x[4, 5::8192] += 20                                # all of them one thread's
+    x[5] = np.arange(V) // 8192                        # each pass above the last
+    x[6] = np.sort(x[6])[::-1]
+    x[7, :100000] = -np.inf
+    run(x, rng.integers(0, V, (8, 1)), top, workspace=torch.zeros(bq.LOGPROBS_COUNTER_BYTES, dtype=torch.uint8, device="cuda"))
+
+
 @pytest.mark.parametrize("dtype", [np.float16, np.float32])
 def test_masked_infinite_and_missing_values(dtype):
     rng = np.random.default_rng(2)
