@@ -412,6 +412,11 @@ __device__ __forceinline__ uint64_t kv_row_bits(const KvAttnMore& p, const KvSeq
   const bool ok = row < rows;
   return kv_row_bits(p, s, kv_row_more(p, s, ok ? row / p.group : 0, ok), j0, left);
 }
+// A score where its bit is set, else -infinity.
+__device__ __forceinline__ float kv_seen(uint64_t bits, int bit, float y) {
+  const uint32_t all = (uint32_t)__builtin_amdgcn_sbfe((int)(bit < 32 ? (uint32_t)bits : (uint32_t)(bits >> 32)), bit & 31, 1);
+  return __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, y) & all) | (0xFF800000u & ~all));
+}
 
 // Floats of a part's result: (max, sum) of each row, then O [ROWS][D].
 __host__ __device__ constexpr int kv_part_floats(int rows, int D) { return rows * (D + 2); }
@@ -632,7 +637,7 @@ __global__ __launch_bounds__(64 * kv_waves(D)) void kv_attn_rows_kernel(P p) {
           for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              y[t][i][e] = (bits >> (16 * i + e)) & 1 ? y[t][i][e] : -__builtin_inff();
+              y[t][i][e] = kv_seen(bits, 16 * i + e, y[t][i][e]);
         }
       } else {
 #pragma unroll

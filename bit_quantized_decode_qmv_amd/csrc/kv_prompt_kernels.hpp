@@ -250,7 +250,7 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void kv_attn_prom
             for (int i = 0; i < 4; ++i)
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                y[t][i][e] = (bits >> (16 * i + e)) & 1 ? y[t][i][e] * c[i] : -__builtin_inff();
+                y[t][i][e] = kv_seen(bits, 16 * i + e, y[t][i][e] * c[i]);
           }
         } else {
 #pragma unroll
