@@ -24,8 +24,8 @@
 // with both in one).  Measured, int8, 48 heads over 8 of 128: one token each of
 // eight sequences, a window of 4096 and 4 sinks 20 us (3.4 TB/s: two or three
 // pages a wave do not hide the start and the join), 2047 rows with a window of
-// 1024 87 (0.59 PFLOP/s: 768 workgroups for the 512 that run at once, and two
-// pages of 18 seen in part), a tree of 13 rows over 1003 tokens 15 (a chain of
+// 1024 86 (0.60 PFLOP/s: 768 workgroups for the 512 that run at once, and two
+// pages of 18 seen in part), a tree of 13 rows over 1003 tokens 14 (a chain of
 // latencies and the join's launch), of 64 over 131001 235 (0.87 PFLOP/s); 16
 // trees of 61 rows over 1024 to 16384 tokens in e4m3 199 (0.69 PFLOP/s: parts of
 // a few pages, the codes' conversion, and 16 us of the join).
@@ -238,6 +238,13 @@ __device__ __forceinline__ bool kv_attn_work(const P& p, int item, KvWork& w) {
       for (int base = 0; base < batch; base += 64) count += __builtin_amdgcn_readlane(kv_scan(tiles(seq(base))), 63);
       const unsigned most = 32u * (unsigned)max(count, 1);
       w.chunk = max(w.chunk, (int)(((unsigned)all + most - 1) / most));
+      // One page each where a tile has 16 parts at most, which the join reads in
+      // two rounds, and all heads have half a chip's.  Measured, us with two pages
+      // and with one: 13 rows of 48 heads over 8 and 1003 tokens 14.8 and 14.0, 26
+      // over 500 16.1 and 14.7, 61 rows of 16 over 8 of 64 and 1003 14.1 and 12.6;
+      // beyond that 13 rows over 1200 14.9 and 16.0, 61 over 1003 19.5 and 22.6.
+      if (all <= 16 * count && (unsigned)all * (unsigned)p.kv_heads <= 128u)
+        w.chunk = max((int)(((unsigned)all + p.target - 1) / (unsigned)p.target), 1);
       // From 12 pages on somewhat longer parts, if all of them then run at
       // once.  Measured, us without and with that: 64 rows of 48 heads over
       // 131001 tokens 250 and 233, 61 rows over 60000 129 and 118, of eight
