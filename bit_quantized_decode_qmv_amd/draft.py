@@ -143,7 +143,7 @@ def logprobs(logits, tokens=None, top: int = 0, entropy: bool = False, workspace
         _gpu(tokens, "tokens")
         if tokens.dim() not in (1, 2):
             raise ValueError(f"tokens have shape {tuple(tokens.shape)}, expected [{rows}] or [{rows}][count]")
-        count = 1 if tokens.dim() == 1 else tokens.shape[1]
+        count = 1 if tokens.dim() == 1 else _kv._int(tokens.shape[1], "count")
         _ints(tokens, "tokens", dev, *((rows,) if tokens.dim() == 1 else (rows, count)))
         logprob = torch.empty(tokens.shape, dtype=torch.float32, device=dev)
     if entropy:

@@ -408,8 +408,8 @@ def kv_attn_tree(cache: KVCache, layer: int, q, cu, lens, table, mask, scale: Op
     _need(mask, "mask", _torch.int64, dev)
     if mask.dim() != 2 or mask.shape[0] != q.shape[0]:
         raise ValueError(f"mask has shape {tuple(mask.shape)}, expected [{q.shape[0]}][words]")
-    return _attn("bq_kv_attn_tree", cache, layer, q, cu, lens, table, scale, out, workspace, (mask.data_ptr(), mask.shape[1]),
-                 (_window(window, "window"), _window(sinks, "sinks")))
+    return _attn("bq_kv_attn_tree", cache, layer, q, cu, lens, table, scale, out, workspace,
+                 (mask.data_ptr(), _int(mask.shape[1], "mask's words")), (_window(window, "window"), _window(sinks, "sinks")))
 
 
 def _window(value, name):
@@ -449,7 +449,7 @@ def kv_keep(cache: KVCache, cu, lens, table, path, kept) -> None:
         raise ValueError(f"path has shape {tuple(path.shape)}, expected [{batch}][max_path]")
     _ints(kept, "kept", dev, batch)
     _launch(dev, "bq_kv_keep", cache.desc, cu.data_ptr(), lens.data_ptr(), table.data_ptr(), batch, max_pages,
-            path.data_ptr(), path.shape[1], kept.data_ptr())
+            path.data_ptr(), _int(path.shape[1], "path's length"), kept.data_ptr())
 
 
 def _ints(t, name, device, *shape):
