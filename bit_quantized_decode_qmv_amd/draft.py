@@ -70,12 +70,12 @@ def _gpu(t, name):
 def _sequences(parent, cu, lens):
     """(device, batch, total)"""
     dev = _gpu(parent, "parent")
+    _kv._need(lens, "lens", _kv._torch.int32, dev)
     if parent.dim() != 1 or lens.dim() != 1:
         raise ValueError(f"expected parent [total], lens [batch]; got {tuple(parent.shape)}, {tuple(lens.shape)}")
     total, batch = parent.shape[0], lens.shape[0]
     _kv._int(total, "total")
     _ints(parent, "parent", dev, total)
-    _ints(lens, "lens", dev, batch)
     _ints(cu, "cu", dev, batch + 1)
     return dev, batch, total
 

@@ -391,10 +391,10 @@ def kv_attn(cache: KVCache, layer: int, q, cu, lens, table, scale: Optional[floa
     for later calls (see bq_kv_attn_workspace); allocated here when None."""
     window = _window(window, "window")
     if not sinks:
-        return _attn("bq_kv_attn", cache, layer, q, cu, lens, table, scale, out, workspace, (), (window, KV_CAUSAL if causal else 0))
+        return _attn("bq_kv_attn", cache, layer, q, cu, lens, table, scale, out, workspace, None, (window, KV_CAUSAL if causal else 0))
     if not causal:
         raise ValueError("sinks need causal")
-    return _attn("bq_kv_attn_sinks", cache, layer, q, cu, lens, table, scale, out, workspace, (), (window, _window(sinks, "sinks")))
+    return _attn("bq_kv_attn_sinks", cache, layer, q, cu, lens, table, scale, out, workspace, None, (window, _window(sinks, "sinks")))
 
 
 def kv_attn_tree(cache: KVCache, layer: int, q, cu, lens, table, mask, scale: Optional[float] = None, window: int = 0,
@@ -403,23 +403,24 @@ def kv_attn_tree(cache: KVCache, layer: int, q, cu, lens, table, mask, scale: Op
     mask int64 [total][words] (tree_plan() makes it) says which rows of its
     sequence a row sees, beside the context ahead of them (window > 0: the
     last window less the rows it sees, and the first `sinks`)."""
-    dev = cache.device
-    _torch or _use_torch()
-    _need(mask, "mask", _torch.int64, dev)
-    if mask.dim() != 2 or mask.shape[0] != q.shape[0]:
-        raise ValueError(f"mask has shape {tuple(mask.shape)}, expected [{q.shape[0]}][words]")
-    return _attn("bq_kv_attn_tree", cache, layer, q, cu, lens, table, scale, out, workspace,
-                 (mask.data_ptr(), _int(mask.shape[1], "mask's words")), (_window(window, "window"), _window(sinks, "sinks")))
+    return _attn("bq_kv_attn_tree", cache, layer, q, cu, lens, table, scale, out, workspace, mask,
+                 (_window(window, "window"), _window(sinks, "sinks")), tree=True)
 
 
 def _window(value, name):
     return _int(min(value, (1 << 31) - 1), name)
 
 
-def _attn(name, cache, layer, q, cu, lens, table, scale, out, workspace, mask, seen):
+def _attn(name, cache, layer, q, cu, lens, table, scale, out, workspace, mask, seen, tree=False):
     dev = cache.device
     stride = _rows(q, "q", dev, None, cache.head_dim)
     total, heads, dim = q.shape
+    words = ()
+    if tree:
+        _need(mask, "mask", _torch.int64, dev)
+        if mask.dim() != 2 or mask.shape[0] != total:
+            raise ValueError(f"mask has shape {tuple(mask.shape)}, expected [{total}][words]")
+        words = (mask.data_ptr(), _int(mask.shape[1], "mask's words"))
     batch, max_pages = _batch(cu, lens, table, dev)
     out, out_stride = _out(out, "out", q, dev)
     ws, ws_bytes = None, 0
@@ -432,7 +433,7 @@ def _attn(name, cache, layer, q, cu, lens, table, scale, out, workspace, mask, s
     if workspace is not None:
         ws = workspace.data_ptr()
     _launch(dev, name, cache.desc, _int(layer, "layer"), q.data_ptr(), out.data_ptr(), stride, out_stride, heads,
-            cu.data_ptr(), lens.data_ptr(), table.data_ptr(), batch, max_pages, total, *mask,
+            cu.data_ptr(), lens.data_ptr(), table.data_ptr(), batch, max_pages, total, *words,
             dim ** -0.5 if scale is None else scale, *seen, ws, ws_bytes)
     return out
 

@@ -34,3 +34,18 @@ def test_tokens_of_a_row(calls):  # noqa: F811
     with pytest.raises(ValueError, match="count"):
         bq.logprobs(far(3, 9), wide(3, torch.int32), workspace=far(64, dtype=torch.uint8))
     assert not calls.noted
+
+
+def test_what_is_no_tensor(calls, cache):  # noqa: F811
+    """Refused as such, whichever argument it is."""
+    ok = dict(q=far(5, 4, 64), cu=ints(3), lens=ints(2), table=ints(2, 4), mask=far(5, 1, dtype=torch.int64))
+    for name in ok:
+        with pytest.raises(TypeError, match=name):
+            bq.kv_attn_tree(cache, 0, **{**ok, name: None}, workspace=far(64, dtype=torch.uint8))
+    ok = dict(parent=ints(5), cu=ints(3), lens=ints(2))
+    for name in ok:
+        with pytest.raises(TypeError, match=name):
+            bq.tree_plan(**{**ok, name: None})
+        with pytest.raises(TypeError, match=name):
+            bq.tree_accept(ints(5), ints(5), **{**ok, name: None}, max_path=3)
+    assert not calls.noted
