@@ -2,6 +2,7 @@
 // writing and reading.  Declarations are in include/bq.h.
 #include <algorithm>
 #include <cmath>
+#include <limits>
 
 #include "kv_cache_kernels.hpp"
 
@@ -38,6 +39,13 @@ int rope_tokens_per_wg(int tokens, int rot_dim, int units, int threads) {
 int check_norm(const float* w, float eps) {
   if (!kv_aligned(w, 4)) return BQ_ERR_ALIGN;
   return std::isfinite(eps) && eps >= 0.f ? BQ_OK : BQ_ERR_SHAPE;
+}
+
+// The hardware's reciprocal root takes a number below the normal ones as 0, and
+// a row of zeros times its infinity would be no number.  The mean of squares of
+// any other fp16 row is at least 2^-58: such an eps is not seen in it.
+NormWeight norm_of(const float* w, float eps) {
+  return NormWeight{w, eps > 0.f ? std::max(eps, std::numeric_limits<float>::min()) : 0.f};
 }
 
 template <bool NORM>
@@ -140,7 +148,7 @@ int bq_norm_rope(const void* x, void* y, long long x_stride, long long y_stride,
   NormRopeParams p{};
   p.rows = RopeRows{static_cast<const _Float16*>(x), static_cast<_Float16*>(y), x_stride, y_stride, heads, head_dim};
   p.a = angles(pos, inv_freq, axis, rot_dim, axes, flags, tokens);
-  p.norm = NormWeight{weight, eps};
+  p.norm = norm_of(weight, eps);
   p.tokens_per_wg = rope_tokens_per_wg(tokens, rot_dim, heads * norm_lanes(head_dim), 256);
   return kv_launch(reinterpret_cast<const void*>(&norm_rope_kernel),
                    dim3((unsigned)((tokens + p.tokens_per_wg - 1) / p.tokens_per_wg)), dim3(256), 0, stream, &p);
@@ -164,8 +172,8 @@ int bq_kv_append_norm(const bq_kv_cache* cache, int layer, const void* k, const 
   if (st == BQ_OK) st = check_norm(q_weight, eps);
   if (st != BQ_OK) return st;
   return append(cache, layer, k, v, k_stride, v_stride, q, q_out, q_stride, q_out_stride, q_heads, cu, lens, table,
-                batch, max_pages, total, pos, inv_freq, axis, rot_dim, axes, flags, NormWeight{k_weight, eps},
-                NormWeight{q ? q_weight : nullptr, eps}, stream);
+                batch, max_pages, total, pos, inv_freq, axis, rot_dim, axes, flags, norm_of(k_weight, eps),
+                norm_of(q ? q_weight : nullptr, eps), stream);
 }
 
 int bq_kv_read(const bq_kv_cache* cache, int layer, void* k, void* v, const int* cu, const int* lens, const int* table,

@@ -18,7 +18,9 @@
 // clears the block's tokens past len.
 //
 // Norms: where a row is normed first, x is x * rsqrt(mean(x^2) + eps) * w over
-// its head's dimensions, in fp32 and without a rounding of its own.
+// its head's dimensions, in fp32 and without a rounding of its own.  The root
+// comes first: x times it is at most sqrt(head_dim), while the root of a small
+// row times a weight may pass fp32's range, and where x is 0 be no number.
 #pragma once
 
 #include <type_traits>
@@ -241,7 +243,7 @@ __device__ __forceinline__ void norm_rope_rows(const RopeRows& p, const RopeAngl
       const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(sum, mean, norm.eps));
       if (!mine || i0 + k * threads >= all) continue;
 #pragma unroll
-      for (int j = 0; j < 16; ++j) y[j] *= r * w[j];
+      for (int j = 0; j < 16; ++j) y[j] = y[j] * r * w[j];
       if (turns) {
         float2 cs[8];
 #pragma unroll
@@ -448,7 +450,7 @@ __global__ __launch_bounds__(PER == 4 ? 512 : 1024) void kv_append_kernel(
           for (int j = 0; j < 16; j += 4) {
             const f32x4 w = *reinterpret_cast<const f32x4*>(&weight[j < 8 ? lo + j : hi + j - 8]);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) x[i][j + k] *= r * w[k];
+            for (int k = 0; k < 4; ++k) x[i][j + k] = x[i][j + k] * r * w[k];
           }
         }
       }
