@@ -59,6 +59,7 @@ struct KvAttnMore : KvAttnParams {
 };
 
 constexpr int kKvMaxParts = 128;  // of a tile
+constexpr int kKvOnePage = 16;    // pages of tiles whose parts may be a page each
 
 // Probabilities enter the second product as fp16 numbers.  They are formed as
 // 2^(score - maximum + kKvLift) and, between two looks at the maximum, grow to
@@ -202,7 +203,19 @@ __device__ __forceinline__ bool kv_attn_work(const P& p, int item, KvWork& w) {
     // the batch's tiles times pages over the target: a long sequence gets as
     // many more parts as it has more pages
     int all = 0;
-    for (int base = 0; base < batch; base += 64) all += tiles(seq(base)) * pages(seq(base));
+    [[maybe_unused]] int count = 0;     // tiles, of which
+    [[maybe_unused]] uint64_t far = 0;  // some have more than kKvOnePage pages
+    for (int base = 0; base < batch; base += 64) {
+      if constexpr (ROWS > 32 && std::is_same_v<P, KvAttnMore>) {
+        const KvSeq s = seq(base);
+        const int n = tiles(s), each = pages(s);
+        all += n * each;
+        count += n;
+        far |= __ballot(n > 0 && each > kKvOnePage);
+      } else {
+        all += tiles(seq(base)) * pages(seq(base));
+      }
+    }
     if (__ballot(falls) != 0) return false;
     all = __builtin_amdgcn_readlane(kv_scan(all), 63);
     // few rows: no part shorter than pays for joining it.  Measured, heads of
@@ -234,16 +247,20 @@ __device__ __forceinline__ bool kv_attn_work(const P& p, int item, KvWork& w) {
       // 17.6 and 23.1, over 4000 17.9, 18.8 and 23.2, four trees over up to
       // 2000 17.8, 18.8 and 23.8; 61 rows of 16 heads of 64 over 16000 (250
       // pages) 27.4, 27.7 and 24.1.
-      int count = 0;
-      for (int base = 0; base < batch; base += 64) count += __builtin_amdgcn_readlane(kv_scan(tiles(seq(base))), 63);
+      count = __builtin_amdgcn_readlane(kv_scan(count), 63);
       const unsigned most = 32u * (unsigned)max(count, 1);
       w.chunk = max(w.chunk, (int)(((unsigned)all + most - 1) / most));
-      // One page each where a tile has 16 parts at most, which the join reads in
-      // two rounds, and all heads have half a chip's.  Measured, us with two pages
-      // and with one: 13 rows of 48 heads over 8 and 1003 tokens 14.8 and 14.0, 26
-      // over 500 16.1 and 14.7, 61 rows of 16 over 8 of 64 and 1003 14.1 and 12.6;
-      // beyond that 13 rows over 1200 14.9 and 16.0, 61 over 1003 19.5 and 22.6.
-      if (all <= 16 * count && (unsigned)all * (unsigned)p.kv_heads <= 128u)
+      // One page each where no tile has more than 16 and all heads together have
+      // half a chip's.  Measured, us with two pages and with one: 13 rows of 48
+      // heads over 8 and 1003 tokens (16 pages) 14.2 and 13.7, over 17 to 19
+      // pages 13.5 to 14.5 and 14.4 to 14.7, 26 over 500 tokens 16.1 and 14.7, 61
+      // of 16 over 8 of 64 and 1003 14.1 and 12.6, 61 over 1003 19.5 and 22.6; 26
+      // rows of 16 over 4 heads of 192 and 4, 8, 12 and 16 pages 17.8, 18.2, 18.9,
+      // 19.1 and 16.3, 17.3, 18.1, 18.9, of 256 20.4, 20.9, 21.5, 22.1 and 18.7,
+      // 19.9, 21.0, 22.3 (13 of 48 over 8 and 16 pages 20.3 and 21.3, the one side
+      // on which it loses); four sequences of 61, 1, 1 and 1 pages, 12 over 2 heads
+      // of 128, 17.7 and 21.3, which is why the longest counts.
+      if (far == 0 && (unsigned)all * (unsigned)p.kv_heads <= 128u)
         w.chunk = max((int)(((unsigned)all + p.target - 1) / (unsigned)p.target), 1);
       // From 12 pages on somewhat longer parts, if all of them then run at
       // once.  Measured, us without and with that: 64 rows of 48 heads over

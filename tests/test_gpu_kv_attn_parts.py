@@ -76,3 +76,24 @@ def test_long_parts(kind, fmt, D, heads, group, lens, news, window, sinks, targe
     check(out.cpu().numpy(), c, 1, table, lens, cu, q, D ** -0.5, seen)
     assert torch.equal(out, call())
     assert bool((guarded[size:] == 255).all()) and not bool(guarded[:bq.KV_ATTN_COUNTER_BYTES].any())
+
+
+@pytest.mark.parametrize("pages,parts", [([16, 1, 1], 16), ([17, 1, 1], 9), ([61, 1, 1, 1], 31), ([16, 16], 32)])
+def test_parts_of_a_page(pages, parts):
+    """A part is one page where no tile has more than 16, however few the others have: a tile of more is not cut into as
+    many parts as it has pages.  Parts of a head are counted by what they leave in the workspace."""
+    import bit_quantized_decode_qmv_amd as bq
+    torch = torch_mod()
+    rng = np.random.default_rng(sum(pages))
+    lens, news, D = [64 * p - 3 for p in pages], [13] * len(pages), 64
+    c, table, q, cu = make(rng, "int8", D, 2, 6, lens, news)
+    args = (upload_cache(c), 1, up(q), up(cu), up(lens, np.int32), up(table))
+    parents = [synth.make_tree(rng, n, 4) for n in news]
+    mask, _ = bq.tree_plan(up(np.concatenate(parents), np.int32), args[3], args[4])
+    slot = 128 * (D + 2) * 4
+    workspace = torch.full((bq.KV_ATTN_COUNTER_BYTES + 200 * slot,), 255, dtype=torch.uint8, device="cuda:0")
+    workspace[:bq.KV_ATTN_COUNTER_BYTES] = 0
+    out = bq.kv_attn_tree(*args, mask, workspace=workspace).cpu().numpy()
+    check(out, c, 1, table, lens, cu, q, D ** -0.5, [oracle.tree_context(13, m - 13, oracle.tree_seen(p)) for p, m in zip(parents, lens)])
+    written = (workspace[bq.KV_ATTN_COUNTER_BYTES:].view(200, slot) != 255).any(1)
+    assert int(written.sum()) == 2 * parts
