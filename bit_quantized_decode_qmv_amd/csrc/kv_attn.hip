@@ -11,7 +11,7 @@ int bq_kv_attn_workspace(const bq_kv_cache* cache, int q_heads, int batch, int t
   *bytes = 0;
   const int st = kv_check_attn(cache, q_heads, batch, total);
   if (st != BQ_OK) return st;
-  const KvAttnPlan p = kv_attn_plan<KvAttnParams>(cache, q_heads, batch, total, 1, SIZE_MAX);
+  const KvAttnPlan p = kv_attn_plan(cache, q_heads, batch, total, 1, SIZE_MAX);
   *bytes = p.bytes;
   return BQ_OK;
 }

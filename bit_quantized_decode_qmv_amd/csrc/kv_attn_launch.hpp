@@ -56,8 +56,8 @@ struct KvAttnPlan {
   int64_t tiles, target;
   size_t bytes;
 };
-template <typename P>
-KvAttnPlan kv_attn_plan(const bq_kv_cache* c, int q_heads, int batch, int total, int64_t max_pages, size_t workspace_bytes) {
+// One plan for both kinds of parameters: bq_kv_attn_workspace gives the size for either.
+inline KvAttnPlan kv_attn_plan(const bq_kv_cache* c, int q_heads, int batch, int total, int64_t max_pages, size_t workspace_bytes) {
   KvAttnPlan p{};
   // By the rows of a sequence, on average; two row groups of wide heads do
   // not fit a wave's registers.  Tiles of 32 for up to 128 rows instead:
@@ -138,7 +138,7 @@ int kv_attn_run(P p, const bq_kv_cache* cache, int layer, const void* q, void* o
   p.causal = flags & BQ_KV_CAUSAL;
   p.window = std::min(window, 1 << 30);  // no sequence is longer; a row's place may be negative
   p.scale = scale * 1.44269504f;
-  const KvAttnPlan pl = kv_attn_plan<P>(cache, q_heads, batch, total, max_pages, workspace ? workspace_bytes : 0);
+  const KvAttnPlan pl = kv_attn_plan(cache, q_heads, batch, total, max_pages, workspace ? workspace_bytes : 0);
   p.target = (int)pl.target;
   // (many rows, measured: parts of 4 pages are 17% faster than of 8 at D 64,
   // 13% slower at D 128.  Wide heads, 4 with 6 query heads each, us in parts of
