@@ -51,12 +51,6 @@ def bq_logprobs_workspace(rows, V, logits_dtype, top):
     return n.value
 
 
-def _ints(t, name, device, *shape):
-    _kv._need(t, name, _kv._torch.int32, device)
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-
-
 def _gpu(t, name):
     """The tensor's device, which has to be a GPU."""
     torch = _kv._torch or _kv._use_torch()
@@ -75,8 +69,8 @@ def _sequences(parent, cu, lens):
         raise ValueError(f"expected parent [total], lens [batch]; got {tuple(parent.shape)}, {tuple(lens.shape)}")
     total, batch = parent.shape[0], lens.shape[0]
     _kv._int(total, "total")
-    _ints(parent, "parent", dev, total)
-    _ints(cu, "cu", dev, batch + 1)
+    _kv._ints(parent, "parent", dev, total)
+    _kv._ints(cu, "cu", dev, batch + 1)
     return dev, batch, total
 
 
@@ -104,8 +98,8 @@ def tree_accept(target, token, parent, cu, lens, max_path: int):
     target, token, parent: int32 [total], target[row] the token that the target
     model has after the row, token[row] the row's own."""
     dev, batch, total = _sequences(parent, cu, lens)
-    _ints(target, "target", dev, total)
-    _ints(token, "token", dev, total)
+    _kv._ints(target, "target", dev, total)
+    _kv._ints(token, "token", dev, total)
     if not 1 <= max_path <= _kv.TREE_MAX_ROWS:
         raise ValueError(f"max_path = {max_path}, expected 1 .. {_kv.TREE_MAX_ROWS}")
     path = parent.new_empty((batch, max_path))
@@ -144,7 +138,7 @@ def logprobs(logits, tokens=None, top: int = 0, entropy: bool = False, workspace
         if tokens.dim() not in (1, 2):
             raise ValueError(f"tokens have shape {tuple(tokens.shape)}, expected [{rows}] or [{rows}][count]")
         count = 1 if tokens.dim() == 1 else _kv._int(tokens.shape[1], "count")
-        _ints(tokens, "tokens", dev, *((rows,) if tokens.dim() == 1 else (rows, count)))
+        _kv._ints(tokens, "tokens", dev, *((rows,) if tokens.dim() == 1 else (rows, count)))
         logprob = torch.empty(tokens.shape, dtype=torch.float32, device=dev)
     if entropy:
         entropies = torch.empty(rows, dtype=torch.float32, device=dev)
