@@ -106,7 +106,7 @@ __global__ __launch_bounds__(256) void tree_accept_kernel(TreeAcceptParams p) {
     found = n;
     p.kept[b] = n;
     p.next_token[b] = n > 0 ? target[last] : -1;
-    p.want[b] = s.n > 0 ? s.base + n : p.t.lens[b];
+    p.want[b] = s.n > 0 ? min(s.base + n, max(p.t.lens[b], 0)) : p.t.lens[b];
   }
   __syncthreads();
   for (int i = (int)threadIdx.x; i < p.max_path; i += 256) p.path[(int64_t)b * p.max_path + i] = i < found ? path[i] : -1;

@@ -530,8 +530,8 @@ int bq_kv_attn_tree(const bq_kv_cache* cache, int layer, const void* q, void* ou
 /* tree_plan -- of every row the rows that it sees, itself and those above it
  * (with window > 0 only the nearest `window` of them), as mask uint64
  * [total][mask_words] for bq_kv_attn_tree, and its position for the rotation,
- * pos int32 [total]: lens[b] - n + the number of rows above it.  mask or pos
- * may be NULL (not both).  Rows past 64 * mask_words of a sequence see
+ * pos int32 [total]: lens[b] - n (at least 0) + the number of rows above it.
+ * mask or pos may be NULL (not both).  Rows past 64 * mask_words of a sequence see
  * nothing and stand at its first row's position.
  *
  * tree_accept -- the path that the target tokens take from row 0 on: of the
@@ -542,7 +542,8 @@ int bq_kv_attn_tree(const bq_kv_cache* cache, int layer, const void* q, void* ou
  *   path [batch][max_path]  the rows taken, rising, then -1; path[0] = 0
  *   kept [batch]            their number, at most max_path
  *   next_token [batch]      the target behind the last of them
- *   want [batch]            lens[b] - n + kept, the length for bq_kv_resize
+ *   want [batch]            lens[b] - n + kept, the length for bq_kv_resize (of
+ *                           fewer tokens than rows: kept, lens[b] at most)
  * A sequence without rows: kept 0, next_token -1, want lens[b].  Rows past
  * BQ_TREE_MAX_ROWS are never taken.  1 <= max_path <= BQ_TREE_MAX_ROWS.
  *
