@@ -402,7 +402,8 @@ def kv_attn_tree(cache: KVCache, layer: int, q, cu, lens, table, mask, scale: Op
     """kv_attn() where the rows of each sequence are a tree of drafted tokens:
     mask int64 [total][words] (tree_plan() makes it) says which rows of its
     sequence a row sees, beside the context ahead of them (window > 0: the
-    last window less the rows it sees, and the first `sinks`)."""
+    last window less the rows it sees, and the first `sinks`, of the context
+    only: rows of the tree are seen as the mask says)."""
     return _attn("bq_kv_attn_tree", cache, layer, q, cu, lens, table, scale, out, workspace, mask,
                  (_window(window, "window"), _window(sinks, "sinks")), tree=True)
 
@@ -442,7 +443,9 @@ def kv_keep(cache: KVCache, cu, lens, table, path, kept) -> None:
     """Moves, over all layers, the keys and values of the rows path[b][i], i <
     kept[b], of each sequence's last cu[b+1] - cu[b] tokens to the places of
     the rows i (path int32 [batch][max_path], kept int32 [batch], as
-    tree_accept() gives them).  kv_resize() to its `want` then cuts the rest."""
+    tree_accept() gives them).  kv_resize() to its `want` then cuts the rest.
+    Older tokens of a block of 16 that takes one with a larger scale are rounded
+    to that scale, as by kv_append()."""
     dev = cache.device
     batch, max_pages = _batch(cu, lens, table, dev)
     _need(path, "path", _torch.int32, dev)

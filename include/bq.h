@@ -514,7 +514,11 @@ int bq_kv_append_norm(const bq_kv_cache* cache, int layer, const void* k, const 
  * and the first `sinks`.  mask uint64 [total][mask_words], 8-byte aligned, 1
  * <= mask_words <= BQ_TREE_MAX_WORDS; rows past 64 * mask_words of a sequence
  * are seen by none.  A row that sees nothing gives zeros.  bq_tree_plan makes
- * the masks of a tree; a mask need not be one of a tree.
+ * the masks of a tree; a mask need not be one of a tree.  The sinks end with the
+ * context: rows of the tree are seen as the mask says and not otherwise.  A
+ * chain over a context shorter than `sinks`, longer than the window and with the
+ * masks of bq_tree_plan, so sees fewer of its own first tokens than the same
+ * rows in bq_kv_attn_sinks, until they are context.
  *
  * Both: arguments, workspace, numerics and errors otherwise as bq_kv_attn
  * (sinks < 0: BQ_ERR_SHAPE). */
@@ -550,9 +554,12 @@ int bq_kv_attn_tree(const bq_kv_cache* cache, int layer, const void* q, void* ou
  * kv_keep -- over all layers, keys and values of the rows path[b][i], i <
  * kept[b], go to the places of the rows i: with bq_kv_resize to `want` they
  * are then the sequence's last tokens.  A block that takes a token gets the
- * largest of its own scale and its tokens' scales; its codes are brought to it
- * (rne; unchanged when the scale did not grow), so every token that no other
- * replaces keeps its value.  lens still counts all n rows.  A sequence whose
+ * largest of its own scale and its tokens' scales, and the codes of tokens that
+ * had a smaller one are brought to it (rne).  So tokens of the block that no
+ * other replaces keep their values only where its scale did not grow; where it
+ * did, they are rounded once more, by half a step of the new scale at most, as
+ * kv_append rounds the older tokens of a block.  Blocks that take no token stay
+ * as they are.  lens still counts all n rows.  A sequence whose
  * path does not rise from row to row inside 0 .. n - 1, or that holds fewer
  * tokens than rows, is left as it is; a row whose page, or whose place's, is
  * missing is not moved.  Pages that are written must not be
