@@ -21,14 +21,19 @@
 // that some row does not see whole: a row's 64 bits of such a page instead of
 // one range.  They are instances of their own, since what the plain ones hold in
 // registers all along leaves no room (rows<128, e4m3, 2> spilled 15 registers
-// with both in one).  Measured, int8, 48 heads over 8 of 128: one token each of
+// with both in one; of their own one instance spills, rows<128, int8, 2>: 4
+// registers, 20 bytes a lane, where the plain one spills 1).  Measured, 48 heads
+// over 8 of 128, int8 unless said: one token each of
 // eight sequences, a window of 4096 and 4 sinks 20 us (3.4 TB/s: two or three
-// pages a wave do not hide the start and the join), 2047 rows with a window of
-// 1024 86 (0.60 PFLOP/s: 768 workgroups for the 512 that run at once, and two
-// pages of 18 seen in part), a tree of 13 rows over 1003 tokens 14 (a chain of
-// latencies and the join's launch), of 64 over 131001 235 (0.87 PFLOP/s); 16
-// trees of 61 rows over 1024 to 16384 tokens in e4m3 199 (0.69 PFLOP/s: parts of
-// a few pages, the codes' conversion, and 16 us of the join).
+// pages a wave do not hide the start and the join), drafts of 5 rows of them 31;
+// 2047 rows with a window of 1024 86 (0.60 PFLOP/s: 768 workgroups for the 512
+// that run at once, and two pages of 18 seen in part); a tree of 5 rows over 1003
+// tokens 15 and over 16384 27, of 32 sequences of 1024 to 16384 133 (4.3 TB/s), of
+// 13 rows over 1003 tokens 14 (a chain of latencies and the join's launch), of 64
+// over 131001 235 (0.87 PFLOP/s); 16 trees of 61 rows over 1024 to 16384 tokens
+// with a window of 1024 and 4 sinks 65, without 335 (0.62 PFLOP/s); with lengths
+// spread over their logarithm, in e4m3, 199 (0.69 PFLOP/s: parts of a few pages,
+// the codes' conversion, and 16 us of the join).
 #pragma once
 
 #include <type_traits>
@@ -239,6 +244,11 @@ __device__ __forceinline__ bool kv_attn_work(const P& p, int item, KvWork& w) {
     // (Where all shares fit one round there is nothing to gain: one head over
     // 2047 pages has parts of 20 pages, 103 of them, 26 us.)
     const unsigned share = ROWS <= 32 ? (unsigned)all + (unsigned)all / 4 : (unsigned)all;
+    // Whatever sets the chunk, here and below, it is ceil(all / target) or more.
+    // So there are `target` parts at most beyond one for each tile, which is what
+    // the launch's grid and the workspace's slots are made for, and a tile has
+    // no more than target <= kKvMaxParts, for which the joins have room: shorter
+    // parts would be written behind the workspace, or not computed.
     w.chunk = max((int)((share + p.target - 1) / (unsigned)p.target), least);
     if constexpr (ROWS > 32 && std::is_same_v<P, KvAttnMore>) {
       // Many rows of a tree, or with sinks: no more than 32 parts of a tile on

@@ -24,9 +24,10 @@
 // bisection, a count over the wave for each step, and the others leave.  A value
 // equal to the floor's passes only with a lower token.  In the end each of the
 // waves' numbers, then of the parts', finds its place by counting those above it.
-// So ties and order change nothing but the time: 2047 rows of 151936 in fp16, top
-// 1, 20 and 64, take 122, 131 and 139 us with random values, 121, 122 and 127 with
-// equal ones, 144, 280 and 843 with values that rise all along.
+// So ties and order change nothing but the time: 2047 rows of 151936 in fp16 with
+// entropy, top 1, 20 and 64, take 118, 127 and 141 us with random values, 125, 128
+// and 133 with equal ones, 116, 120 and 121 with values that fall all along, 144,
+// 288 and 846 with values that rise: each pass then holds only new ones.
 #pragma once
 
 #include "kv_common.hpp"
@@ -294,10 +295,10 @@ __device__ __forceinline__ LpSums lp_join(LpSums x) {
 // are bound by HBM and, not far behind, by issue (a conversion, a product, an
 // exponential and two sums for a value), few by the chain of latencies from the
 // first load to the join.  Measured with entropy, us without alternatives and
-// with 1, 5, 20 and 64: 2047 rows of 151936 in fp16 111, 118, 122, 127 and 140
-// (622 MB: 5.6 to 4.4 TB/s), 301 rows of it 20.7, 27.1, 30.6, 34.7 and 45.4, 5
-// rows 5.3, 9.8, 10.8, 12.0 and 14.3; 301 rows of 32000 in fp32 11.1, 14.8, 16.7,
-// 18.4 and 24.5.  Eight waves a SIMD with alternatives, which take some registers
+// with 1, 5, 20 and 64: 2047 rows of 151936 in fp16 110, 118, 123, 127 and 141
+// (622 MB: 5.65 to 4.4 TB/s; without entropy 107, 113, 117, 124 and 138), 301 rows
+// of it 20.9, 27.6, 30.6, 35.0 and 45.1, 5 rows 5.4, 9.9, 10.9, 12.6 and 14.7; 301
+// rows of 32000 in fp32 11.0, 15.1, 16.7, 18.4 and 24.5.  Eight waves a SIMD with alternatives, which take some registers
 // to memory: 127, 130, 133 and 142 us for the first of these, 30.3, 33.2, 37.8 and
 // 48.9 for the second; five waves 115, 119, 124 and 139, but 2047 rows of 32000
 // take 36.2 for 34.6 (top 5).  The next pass's loads asked for a pass ahead: 132
