@@ -195,7 +195,7 @@ __device__ __forceinline__ float norm_sum(float x, int lanes) {
 // registers, and a row's sum of squares is the work of `lanes` lanes side by
 // side.  Bound by HBM like the rotation alone; the sum is hidden behind the
 // loads of the other rounds.  Measured in a captured run, 48 heads of 128: 8191
-// tokens 35.8 us (5.6 TB/s; the rotation alone 35.2), 5 tokens 4.0 (3.6).
+// tokens 35.6 us (5.6 TB/s; the rotation alone 34.7), 5 tokens 3.7 (3.1).
 __device__ __forceinline__ void norm_rope_rows(const RopeRows& p, const RopeAngles& a, const NormWeight& norm, int token0,
                                                int tokens, int thread, int threads, float2* table) {
   const int half = a.rot >> 1;
@@ -311,7 +311,7 @@ __device__ __forceinline__ void kv_transpose4(const uint32_t (&x)[4], uint32_t (
 // of the barrier that the angles' table needs anyway.  k's weights lie in LDS: a
 // thread holds four tokens in registers already (weights in registers too: 35.4 us
 // for 28.3).  Measured in a captured run, 8 heads of 128 and q of 48: 4093
-// tokens 28.3 us (without norms 25.0), one token each of 32 sequences 8.4 (7.4).
+// tokens 27.4 us (without norms 24.6), one token each of 32 sequences 7.7 (6.8).
 template <int PER, bool NORM = false>
 __global__ __launch_bounds__(PER == 4 ? 512 : 1024) void kv_append_kernel(
     std::conditional_t<NORM, KvAppendNormParams, KvAppendParams> p) {
