@@ -291,21 +291,23 @@ __device__ __forceinline__ LpSums lp_join(LpSums x) {
 
 // One workgroup for a part of a row (of the whole row where rows fill the
 // chip); a row's parts are joined by the one that finishes last.  A wave takes
-// 4 KB at a time; what hides its loads is the other waves of its SIMD.  Many rows
-// are bound by HBM and, not far behind, by issue (a conversion, a product, an
-// exponential and two sums for a value), few by the chain of latencies from the
-// first load to the join.  Measured with entropy, us without alternatives and
-// with 1, 5, 20 and 64: 2047 rows of 151936 in fp16 110, 118, 123, 127 and 141
-// (622 MB: 5.65 to 4.4 TB/s; without entropy 107, 113, 117, 124 and 138), 301 rows
-// of it 20.9, 27.6, 30.6, 35.0 and 45.1, 5 rows 5.4, 9.9, 10.9, 12.6 and 14.7; 301
-// rows of 32000 in fp32 11.0, 15.1, 16.7, 18.4 and 24.5.  Eight waves a SIMD with alternatives, which take some registers
-// to memory: 127, 130, 133 and 142 us for the first of these, 30.3, 33.2, 37.8 and
-// 48.9 for the second; five waves 115, 119, 124 and 139, but 2047 rows of 32000
-// take 36.2 for 34.6 (top 5).  The next pass's loads asked for a pass ahead: 132
-// us (top 5, 16 registers more).  Numbers are ranked by a thread each, and the
-// finding of the `top` largest by bisection stands in three places only: with
-// one wave that put them together first, and eight places, the code was 45 KB
-// for 25, and 5 rows took 13.5 and 19.0 us (top 20 and 64).
+// 4 KB at a time; what hides its loads is the other waves of its SIMD.  Many
+// rows are bound by HBM and, not far behind, by issue (a conversion, a
+// product, an exponential and two sums for a value), few by the chain of
+// latencies from the first load to the join.  Measured with entropy, us
+// without alternatives and with 1, 5, 20 and 64: 2047 rows of 151936 in fp16
+// 110, 118, 123, 127 and 141 (622 MB: 5.65 to 4.4 TB/s; without entropy 107,
+// 113, 117, 124 and 138), 301 rows of it 20.9, 27.6, 30.6, 35.0 and 45.1, 5
+// rows 5.4, 9.9, 10.9, 12.6 and 14.7; 301 rows of 32000 in fp32 11.0, 15.1,
+// 16.7, 18.4 and 24.5.  Eight waves a SIMD with alternatives, which take some
+// registers to memory: 127, 130, 133 and 142 us for the first of these, 30.3,
+// 33.2, 37.8 and 48.9 for the second; five waves 115, 119, 124 and 139, but
+// 2047 rows of 32000 take 36.2 for 34.6 (top 5).  The next pass's loads asked
+// for a pass ahead: 132 us (top 5, 16 registers more).  Numbers are ranked by
+// a thread each, and the finding of the `top` largest by bisection stands in
+// three places only: with one wave that put them together first, and eight
+// places, the code was 45 KB for 25, and 5 rows took 13.5 and 19.0 us (top 20
+// and 64).
 template <typename T, bool ENTROPY, bool TOP>
 __global__ __launch_bounds__(kLpThreads, TOP ? 6 : 8) void logprobs_kernel(LogprobsParams p) {
   constexpr int EPV = 16 / (int)sizeof(T);  // values of a 16-byte block
